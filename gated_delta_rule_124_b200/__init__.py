@@ -19,4 +19,11 @@ from .kda import (  # noqa: F401
     load, status_string, kda_layer_decode_step, kda_test_overlap_flag_timeout,
     kda_layer_chunk_fwd, kda_layer_chunk_fwd_workspace_size, kda_chunk_state_maps,
     kda_fold_segment_states,
+    kda_linear_scan_num_entries, kda_linear_scan_workspace_size,
+    kda_linear_scan_bwd_workspace_size, kda_linear_scan_fwd, kda_linear_scan_bwd,
+    kda_linear_scan_step, linear_scan, linear_scan_bwd, linear_scan_step, LinearScan,
+    gated_linear_scan, kda_fp8_pitch, kda_add_rms_norm, kda_add_rms_norm_bwd,
+    kda_add_rms_norm_bwd_workspace_size, add_rms_norm, add_rms_norm_bwd, AddRMSNorm,
+    residual_rms_norm, kda_quantize_fp8, quantize_fp8, kda_fp8_matmul, fp8_matmul, Fp8Linear,
+    fp8_linear,
 )

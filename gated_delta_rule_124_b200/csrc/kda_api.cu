@@ -182,6 +182,40 @@ Path gdn_path(int total, int N, bool packed, int H, int dk, int dv, int chunk, k
     return select_path(total, N, packed, H, dk, dv, chunk, dt);
 }
 
+// The gated linear recurrence: any H and d whose product the kernels index.
+bool scan_dims_ok(int H, int d) {
+    return H >= 1 && d >= 1 && (long long)H * d <= (1LL << 24);
+}
+// Checks shared by its forward and backward; `need` must be given if there is a
+// token, `may` are NULL or aligned.
+kda_status_t check_scan(const int32_t* cu, int B, int T, int num_seqs, int H, int d,
+                        kda_dtype_t dt, void* ws, size_t bytes, bool backward,
+                        std::initializer_list<const void*> need,
+                        std::initializer_list<const void*> may, Prefill* p) {
+    if (!scan_dims_ok(H, d)) return KDA_ERR_INVALID_ARG;
+    // (dk, dv and the chunk play no part here: any supported ones)
+    const kda_status_t s = check_prefill_shape(cu, B, T, num_seqs, H, 128, 128, 64, dt, p);
+    if (s != KDA_OK) return s;
+    if (p->total > 0x7fffff00) return KDA_ERR_INVALID_ARG;  // token indices stay in 32 bits
+    for (const void* ptr : need)
+        if ((!ptr && p->total > 0) || !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    for (const void* ptr : may)
+        if (ptr && !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    if (!ws) return KDA_ERR_WORKSPACE;
+    if (!aligned256(ws)) return KDA_ERR_INVALID_ARG;
+    if (bytes < kda::scan_workspace_bytes(p->total, H * d, backward)) return KDA_ERR_WORKSPACE;
+    return KDA_OK;
+}
+
+constexpr int kMaxNormDim = 16384;
+constexpr int kMaxFp8Dim = 0x7fffff00;
+kda_status_t check_norm(int rows, int D, kda_dtype_t dt, float eps) {
+    if (rows < 0 || D < 1 || !dtype_ok(dt)) return KDA_ERR_INVALID_ARG;
+    if (!(eps > 0.f) || !(eps < 1e30f)) return KDA_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > kMaxNormDim) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
 size_t gdn_workspace_bytes(const Prefill& p, int H, int dk, int dv, int chunk, Path path,
                            size_t* spread_offset) {
     const size_t base = carve_for(nullptr, p, H, dk, dv, chunk, path).total_bytes;
@@ -839,6 +873,139 @@ kda_status_t kda_layer_decode_step(const void* xq, const void* xk, const void* x
                                               beta, state, gate, w_norm, N, H, dk, dv, dtype,
                                               l2_eps, rms_eps, y,
                                               static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------- gated linear recurrence
+
+int kda_linear_scan_num_entries(int total_tokens) {
+    return total_tokens < 0 ? 0 : static_cast<int>(kda::scan_tiles(total_tokens));
+}
+
+size_t kda_linear_scan_workspace_size(int total_tokens, int H, int d) {
+    if (total_tokens < 0 || !scan_dims_ok(H, d)) return 0;
+    return kda::scan_workspace_bytes(total_tokens, H * d, false);
+}
+
+size_t kda_linear_scan_bwd_workspace_size(int total_tokens, int H, int d) {
+    if (total_tokens < 0 || !scan_dims_ok(H, d)) return 0;
+    return kda::scan_workspace_bytes(total_tokens, H * d, true);
+}
+
+kda_status_t kda_linear_scan_fwd(const void* x, const float* g, const float* initial_state,
+                                 const int32_t* cu_seqlens, int B, int T, int num_seqs, int H,
+                                 int d, kda_dtype_t dtype, void* h, float* final_state,
+                                 float* entry_states, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    Prefill p;
+    kda_status_t s = check_scan(cu_seqlens, B, T, num_seqs, H, d, dtype, workspace,
+                                workspace_bytes, false, {x, g, h},
+                                {initial_state, final_state, entry_states}, &p);
+    if (s != KDA_OK) return s;
+    return from_cuda(kda::launch_scan_fwd(x, g, initial_state, cu_seqlens, T, p.total, p.N, H * d,
+                                          dtype, h, final_state, entry_states, workspace,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+kda_status_t kda_linear_scan_bwd(const void* x, const float* g, const float* initial_state,
+                                 const void* dout, const float* dfinal_state,
+                                 const float* entry_states, const int32_t* cu_seqlens, int B,
+                                 int T, int num_seqs, int H, int d, kda_dtype_t dtype, void* dx,
+                                 float* dg, float* dinitial_state, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    Prefill p;
+    kda_status_t s = check_scan(cu_seqlens, B, T, num_seqs, H, d, dtype, workspace,
+                                workspace_bytes, true, {x, g, dout, dx, dg},
+                                {initial_state, dfinal_state, entry_states, dinitial_state}, &p);
+    if (s != KDA_OK) return s;
+    if (dinitial_state && (dinitial_state == dfinal_state || dinitial_state == initial_state))
+        return KDA_ERR_INVALID_ARG;
+    return from_cuda(kda::launch_scan_bwd(x, g, initial_state, dout, dfinal_state, entry_states,
+                                          cu_seqlens, T, p.total, p.N, H * d, dtype, dx, dg,
+                                          dinitial_state, workspace,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+kda_status_t kda_linear_scan_step(const void* x, const float* g, const float* state_in,
+                                  float* state_out, void* h, int N, int H, int d,
+                                  kda_dtype_t dtype, void* stream) {
+    if (N < 0 || !scan_dims_ok(H, d) || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
+    if (N == 0) return KDA_OK;
+    for (const void* ptr : std::initializer_list<const void*>{x, g, state_in, state_out, h})
+        if (!ptr || !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    return from_cuda(kda::launch_scan_step(x, g, state_in, state_out, (long long)N * H * d, dtype,
+                                           h, static_cast<cudaStream_t>(stream)));
+}
+
+// --------------------------------- pre-norm, 8-bit matrices, projections
+
+int kda_fp8_pitch(int K) { return K < 0 || K > 0x7ffffff0 ? 0 : kda::fp8_pitch(K); }
+
+kda_status_t kda_add_rms_norm(const void* x, const void* residual, const float* w, int rows,
+                              int D, kda_dtype_t dtype, float eps, void* sum, void* y, void* y8,
+                              float* y8_scale, void* stream) {
+    const kda_status_t s = check_norm(rows, D, dtype, eps);
+    if (s != KDA_OK || rows == 0) return s;
+    if ((!y && !y8) || (y8 != nullptr) != (y8_scale != nullptr)) return KDA_ERR_INVALID_ARG;
+    for (const void* ptr : std::initializer_list<const void*>{residual, sum, y, y8, y8_scale})
+        if (ptr && !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    for (const void* ptr : std::initializer_list<const void*>{x, w})
+        if (!ptr || !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    return from_cuda(kda::launch_add_rms_norm(x, residual, w, rows, D, dtype, eps, sum, y, y8,
+                                              y8_scale, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_add_rms_norm_bwd_workspace_size(int rows, int D) {
+    if (check_norm(rows, D, KDA_DTYPE_F32, 1.f) != KDA_OK) return 0;
+    return kda::rms_norm_bwd_workspace_bytes(rows, D);
+}
+
+kda_status_t kda_add_rms_norm_bwd(const void* s, const float* w, const void* dy, const void* dsum,
+                                  int rows, int D, kda_dtype_t dtype, float eps, void* dx,
+                                  float* dw, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+    const kda_status_t st = check_norm(rows, D, dtype, eps);
+    if (st != KDA_OK) return st;
+    for (const void* ptr : std::initializer_list<const void*>{s, dy, dx})
+        if ((!ptr && rows > 0) || !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    for (const void* ptr : std::initializer_list<const void*>{w, dw})
+        if (!ptr || !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    if (dsum && !aligned16(dsum)) return KDA_ERR_INVALID_ARG;
+    if (rows > 0 && (dx == s || dx == dy)) return KDA_ERR_INVALID_ARG;
+    if (!workspace) return KDA_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return KDA_ERR_INVALID_ARG;
+    if (workspace_bytes < kda::rms_norm_bwd_workspace_bytes(rows, D)) return KDA_ERR_WORKSPACE;
+    return from_cuda(kda::launch_add_rms_norm_bwd(s, w, dy, dsum, rows, D, dtype, eps, dx, dw,
+                                                  workspace, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status_t kda_quantize_fp8(const void* x, int rows, int cols, kda_dtype_t dtype,
+                              int block_rows, int transpose, void* y8, float* scale,
+                              void* stream) {
+    if (rows < 0 || cols < 1 || rows > kMaxFp8Dim || cols > kMaxFp8Dim || !dtype_ok(dtype))
+        return KDA_ERR_INVALID_ARG;
+    if (block_rows != 1 && block_rows != 128) return KDA_ERR_UNSUPPORTED;
+    if ((long long)kda::blocks128(rows) * kda::blocks128(cols) > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED;
+    if (rows == 0) return KDA_OK;
+    for (const void* ptr : std::initializer_list<const void*>{x, y8, scale})
+        if (!ptr || !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    return from_cuda(kda::launch_quantize(x, rows, cols, dtype, block_rows == 1, transpose != 0,
+                                          y8, scale, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status_t kda_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
+                            const float* b_scale, int M, int N, int K, int b_block_rows,
+                            kda_dtype_t out_dtype, void* out, void* stream) {
+    if (M < 0 || N < 1 || K < 1 || M > kMaxFp8Dim || N > kMaxFp8Dim || K > kMaxFp8Dim ||
+        !dtype_ok(out_dtype))
+        return KDA_ERR_INVALID_ARG;
+    if (b_block_rows != 1 && b_block_rows != 128) return KDA_ERR_UNSUPPORTED;
+    if (M == 0) return KDA_OK;
+    for (const void* ptr : std::initializer_list<const void*>{a8, a_scale, b8, b_scale, out})
+        if (!ptr || !aligned16(ptr)) return KDA_ERR_INVALID_ARG;
+    if (!kda::fp8_matmul_available()) return KDA_ERR_UNSUPPORTED;
+    return from_cuda(kda::launch_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows == 1,
+                                            out_dtype, out, static_cast<cudaStream_t>(stream)));
 }
 
 // ----------------------------------------------------------------- status

@@ -283,6 +283,41 @@ cudaError_t launch_bwd_head_gate(const void* q, const void* k, const void* v, co
                                  int dv, kda_dtype_t dt, float* dq, float* dkk, float* dvv,
                                  float* dg_head, float* db, float* dh0, void* workspace,
                                  cudaStream_t st);
+// The gated linear recurrence (kda_scan.cu): C = H d channels, entry states of
+// tiles of kScanRows tokens.
+constexpr int kScanRows = 64;
+inline size_t scan_tiles(int total) {
+    return total > 0 ? ((size_t)total + kScanRows - 1) / kScanRows : 1;
+}
+size_t scan_workspace_bytes(int total, int C, bool backward);
+cudaError_t launch_scan_fwd(const void* x, const float* g, const float* h0, const int32_t* cu,
+                            int T, int total, int N, int C, kda_dtype_t dt, void* h,
+                            float* final_state, float* entry, void* workspace, cudaStream_t st);
+cudaError_t launch_scan_bwd(const void* x, const float* g, const float* h0, const void* dout,
+                            const float* dfinal, const float* entry, const int32_t* cu, int T,
+                            int total, int N, int C, kda_dtype_t dt, void* dx, float* dg,
+                            float* dh0, void* workspace, cudaStream_t st);
+cudaError_t launch_scan_step(const void* x, const float* g, const float* state_in,
+                             float* state_out, long long n, kda_dtype_t dt, void* h,
+                             cudaStream_t st);
+// The residual RMS norm and its backward (kda_norm.cu).
+size_t rms_norm_bwd_workspace_bytes(int rows, int D);
+cudaError_t launch_add_rms_norm(const void* x, const void* residual, const float* w, int rows,
+                                int D, kda_dtype_t dt, float eps, void* sum, void* y, void* y8,
+                                float* y8_scale, cudaStream_t st);
+cudaError_t launch_add_rms_norm_bwd(const void* s, const float* w, const void* dy,
+                                    const void* dsum, int rows, int D, kda_dtype_t dt, float eps,
+                                    void* dx, float* dw, void* workspace, cudaStream_t st);
+// 8-bit matrices: rows of fp8_pitch(K) bytes, scales per block of 128 columns
+// (kda_quantize.cu), and their product (kda_fp8_matmul.cu).
+inline int fp8_pitch(int K) { return (K + 15) / 16 * 16; }
+inline int blocks128(int n) { return (n + 127) / 128; }
+cudaError_t launch_quantize(const void* x, int rows, int cols, kda_dtype_t dt, bool row_blocks,
+                            bool transpose, void* y8, float* scale, cudaStream_t st);
+bool fp8_matmul_available();
+cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
+                              const float* b_scale, int M, int N, int K, bool b_rows,
+                              kda_dtype_t out_dt, void* out, cudaStream_t st);
 // G_full[t, h, c] = g[t, h] (a head-uniform gate spread over dk channels)
 cudaError_t launch_spread_gate(const float* g, int total, int H, int dk, float* out,
                                cudaStream_t st);

@@ -1,0 +1,694 @@
+// Gated linear recurrence: h_t = exp(g_t) h_{t-1} + x_t per (sequence, head,
+// channel), its backward pass and its one-token step.
+//
+// The delta-rule operator without the key side (one state value per channel):
+// every (token, channel) is an affine map h -> alpha h + x, and maps compose
+// associatively, (alpha2, x2) o (alpha1, x1) = (alpha1 alpha2, alpha2 x1 + x2),
+// so a long sequence splits over time.  A token is used once (a few flops per
+// 8 bytes), so the kernels are bound by HBM: each element is read once and
+// written once, and the state crosses tiles through a few bytes per channel.
+//
+// Forward: the packed tokens are cut into tiles of kRows = 64 (regardless of
+// sequence bounds) by 128 channels.  A 256-thread CTA holds one tile in
+// registers: lane l of warp w holds channels [4 l, 4 l + 4) of rows [8 w, 8 w + 8),
+// all loads issued at once.  Each warp composes its eight rows, the CTA's
+// eight maps are composed through shared memory, and the tile's entry state
+// comes from a look-back over the tiles before it: each tile publishes its
+// composed map as soon as it has it and its exit state as soon as it knows its
+// entry state, so a tile composes its predecessors' maps until it meets an
+// exit state.  Then every warp runs the recurrence once more from its own
+// entry state, in the order of the definition, and writes h.  The first token
+// of a sequence replaces the state by the initial one, so a tile that holds
+// one knows its exit state without looking back.
+//
+// A published value is one 64-bit word per (tile, channel), written and read
+// with single relaxed accesses, so that no fence is needed: {log2 of the gate
+// product, state part}; two NaN patterns in the first half mark "not yet" and
+// "exit state".  Gate products stay logarithms (their sum in fp32) until they
+// meet a state: exp is split into two factors, so that a product beyond the
+// fp32 range times a small state is still right.
+//
+// Tiles are taken by ticket in the order of the look-back (channels fastest),
+// so a tile only ever waits for tiles that have started.  The waits are
+// bounded all the same.
+//
+// Backward: with e the gradient that reaches the state from the right (the
+// final state's gradient at a sequence's last token),
+//     dh_t = dout_t + e_{t+1},  dx_t = dh_t,  e_t = alpha_t dh_t,
+//     dg_t = e_t h_{t-1},  dh_0 = e at the first token:
+// the same look-back runs from the right for e, and h_{t-1} is recomputed
+// inside each tile from the tile's entry state, which the forward keeps (one
+// fp32 row per 64 tokens).  x, g, dout in and dx, dg out, each once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_common.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kR = 8;                  // rows of a warp
+constexpr int kRows = kR * kWarps;     // rows of a tile
+static_assert(kRows == kScanRows, "the entry states are those of the tiles");
+constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // NaN patterns no sum of logarithms has
+constexpr uint32_t kExit = 0xFFFFFFFEu;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kWindow = 4;             // published words a look-back requests at once
+
+struct ScanArgs {
+    const void* x;
+    const float* g;
+    const float* h0;        // initial states [N, C] or NULL
+    const int32_t* cu;      // packed offsets or NULL
+    int T, total, N, C;
+    void* h;                // forward: [total, C], or NULL (entry states only)
+    float* final_state;     // [N, C] or NULL
+    float* entry;           // [tiles, C]: forward: out or NULL; backward: in
+    const void* dout;       // backward
+    const float* dfinal;    // [N, C] or NULL
+    void* dx;
+    float* dg;
+    float* dh0;             // [N, C] or NULL
+    uint32_t* status;
+    uint32_t* ticket;       // starts at 0xFFFFFFFF; NULL: one tile per channel block
+    uint64_t* words;        // [tiles, C]
+    int tiles, ctiles;
+};
+
+// Four channels (VEC = 4) or one (VEC = 1) of a row; fp32 or bf16.
+template <int VEC, typename T>
+struct Raw;
+template <>
+struct Raw<4, float> {
+    float4 v;
+    __device__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ void load(const float* p) { v = __ldcs(reinterpret_cast<const float4*>(p)); }
+    __device__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+};
+template <>
+struct Raw<4, __nv_bfloat16> {
+    uint2 v;
+    __device__ void zero() { v = make_uint2(0u, 0u); }
+    __device__ void load(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint2*>(p)); }
+    __device__ void get(float (&o)[4]) const {
+        o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+};
+template <typename T>
+struct Raw<1, T> {
+    T v;
+    __device__ void zero() { v = from_f32<T>(0.f); }
+    __device__ void load(const T* p) { v = *p; }
+    __device__ void get(float (&o)[1]) const { o[0] = to_f32(v); }
+};
+
+__device__ __forceinline__ void put(float* p, const float (&o)[4]) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(o[0], o[1], o[2], o[3]));
+}
+__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&o)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2], o[3]);
+    uint2 u;
+    u.x = *reinterpret_cast<const uint32_t*>(&a);
+    u.y = *reinterpret_cast<const uint32_t*>(&b);
+    __stcs(reinterpret_cast<uint2*>(p), u);
+}
+template <typename T>
+__device__ __forceinline__ void put(T* p, const float (&o)[1]) { *p = from_f32<T>(o[0]); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// h times 2^G, also where 2^G alone leaves the fp32 range.
+__device__ __forceinline__ float scaled(float h, float G) {
+    const float e = exp2f(0.5f * G);
+    return h == 0.f ? 0.f : (h * e) * e;  // (0 times a product that overflows is 0)
+}
+// The state after a map (G, b) applied to h; G = -inf: the map forgets h.
+__device__ __forceinline__ float applied(float G, float b, float h) {
+    return G == -INFINITY ? b : b + scaled(h, G);
+}
+
+__device__ __forceinline__ void publish(uint64_t* w, float G, float b, bool exit_state) {
+    const uint32_t lo = exit_state ? kExit : (G != G ? 0x7FFFFFFFu : __float_as_uint(G));
+    const uint64_t v = static_cast<uint64_t>(__float_as_uint(b)) << 32 | lo;
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(w), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint64_t read_word(const uint64_t* w) {
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(w) : "memory");
+    return v;
+}
+
+// The state that enters a tile: composes the maps of the tiles before it (word
+// `first`, then `first + step`, ..., `count` of them) until one has published
+// its exit state; the last of them always does.
+__device__ float look_back(const uint64_t* words, size_t C, int first, int step, int count,
+                           uint32_t* status) {
+    float G = 0.f, h = 0.f;
+    for (int i = 0; i < count; i += kWindow) {
+        uint64_t v[kWindow];
+#pragma unroll
+        for (int j = 0; j < kWindow; ++j)
+            v[j] = read_word(words + (size_t)(first + step * min(i + j, count - 1)) * C);
+#pragma unroll
+        for (int j = 0; j < kWindow; ++j) {
+            if (i + j >= count) return h;
+            if (static_cast<uint32_t>(v[j]) == kNotYet) {
+                const uint64_t t0 = sm100::global_timer_ns();
+                do {
+                    v[j] = read_word(words + (size_t)(first + step * (i + j)) * C);
+                    if (sm100::global_timer_ns() - t0 > kWaitNs) {
+                        atomicOr(status, STATUS_TIMEOUT);
+                        return h;
+                    }
+                } while (static_cast<uint32_t>(v[j]) == kNotYet);
+            }
+            const uint32_t lo = static_cast<uint32_t>(v[j]);
+            const float b = __uint_as_float(static_cast<uint32_t>(v[j] >> 32));
+            h += scaled(b, G);
+            if (lo == kExit) return h;
+            G += __uint_as_float(lo);
+        }
+    }
+    return h;
+}
+
+// Sequence bounds inside the tile's rows: first_of[r] = the sequence whose first
+// token is row r, last_of[r] = the one whose last token it is, -1 elsewhere.
+// Reads of cu stay inside [0, N] and writes inside the tile whatever cu holds.
+__device__ __forceinline__ void mark_bounds(const ScanArgs& a, int t0, int* first_of,
+                                            int* last_of) {
+    for (int r = threadIdx.x; r < kRows; r += kThreads) first_of[r] = last_of[r] = -1;
+    int lo;  // the last sequence whose first token is at or before t0
+    if (!a.cu) {
+        lo = a.T > 0 ? t0 / a.T : 0;
+    } else {  // every warp searches for itself, 32 offsets at a time
+        const int lane = threadIdx.x & 31;
+        lo = 0;
+        int span = a.N;
+        while (true) {
+            const int step = span <= 32 ? 1 : (span + 31) / 32;
+            const int idx = lo + lane * step;
+            const bool le = idx < lo + span && idx < a.N && a.cu[idx] <= t0;
+            const unsigned m = __ballot_sync(0xffffffffu, le);
+            lo += (m ? 31 - __clz(static_cast<int>(m)) : 0) * step;
+            if (step == 1) break;
+            span = min(step, a.N - lo);
+        }
+    }
+    __syncthreads();
+    for (int i = lo + threadIdx.x; i < a.N; i += kThreads) {
+        const int b = (a.cu ? a.cu[i] : i * a.T) - t0;
+        if (b >= kRows) break;
+        const int e = (a.cu ? a.cu[i + 1] : (i + 1) * a.T) - t0;
+        if (e <= b) continue;  // an empty sequence has no token
+        if (b >= 0) first_of[b] = i;
+        if (e >= 1 && e <= kRows) last_of[e - 1] = i;
+    }
+    __syncthreads();
+}
+
+// Whether the offsets run from 0 to total without decreasing: the CTA of the
+// first tile and channels sets the status word (it starts before every CTA
+// that could report a timeout there, and such a report is seconds later).
+__device__ void report_status(const ScanArgs& a) {
+    bool bad = false;
+    if (a.cu) {
+        for (int i = threadIdx.x; i < a.N; i += kThreads) bad |= a.cu[i] > a.cu[i + 1];
+        if (threadIdx.x == 0) bad |= a.cu[0] != 0 || a.cu[a.N] != a.total;
+    }
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *a.status = any ? STATUS_BAD_SEQLENS : 0u;
+}
+
+// States of empty sequences: nothing changes them (channels [c0, c0 + n)).
+__device__ void pass_empty(const ScanArgs& a, const float* from, float* to, int c0, int n) {
+    if (!to) return;
+    for (int i = threadIdx.x / 32; i < a.N; i += kWarps) {
+        const int len = a.cu ? a.cu[i + 1] - a.cu[i] : a.T;
+        if (len > 0) continue;
+        for (int c = threadIdx.x & 31; c < n; c += 32) {
+            const size_t k = (size_t)i * a.C + c0 + c;
+            to[k] = from ? from[k] : 0.f;
+        }
+    }
+}
+
+// The tile this CTA works on, in the order in which tiles wait for one another.
+__device__ __forceinline__ int next_tile(const ScanArgs& a) {
+    if (!a.ticket) return blockIdx.x;
+    __shared__ uint32_t s_ticket;
+    if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u) + 1u;
+    __syncthreads();
+    return static_cast<int>(s_ticket);
+}
+
+template <int VEC, typename T>
+__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanArgs a) {
+    constexpr int CT = 32 * VEC;  // channels of a tile
+    __shared__ __align__(16) float s_G[kWarps][CT], s_b[kWarps][CT];
+    __shared__ int s_first[kRows], s_last[kRows];
+
+    const int task = next_tile(a), tile = task / a.ctiles, c0 = (task % a.ctiles) * CT;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = c0 + lane * VEC, t0 = tile * kRows;
+    const bool mine = c < a.C;
+    const size_t C = a.C;
+
+    // 1. the whole tile into registers
+    Raw<VEC, T> xr[kR];
+    Raw<VEC, float> gr[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int t = t0 + w * kR + r;
+        xr[r].zero();
+        gr[r].zero();
+        if (mine && t < a.total) {
+            xr[r].load(static_cast<const T*>(a.x) + (size_t)t * C + c);
+            gr[r].load(a.g + (size_t)t * C + c);
+        }
+    }
+    mark_bounds(a, t0, s_first, s_last);
+    if (tile == 0) {
+        if (c0 == 0) report_status(a);
+        pass_empty(a, a.h0, a.final_state, c0, min(CT, a.C - c0));
+    }
+
+    // 2. the map of this warp's rows
+    float al[kR][VEC], G[VEC], b[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int first = s_first[w * kR + r];
+        float gv[VEC], xv[VEC];
+        gr[r].get(gv);
+        xr[r].get(xv);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            al[r][j] = expf(gv[j]);
+            G[j] = fmaf(gv[j], kLog2e, G[j]);
+        }
+        if (first >= 0) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                G[j] = -INFINITY;
+                b[j] = a.h0 && mine ? a.h0[(size_t)first * C + c + j] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[r][j], b[j], xv[j]);
+        // from here on a first row's al is its state: initial_state is read
+        // before this tile publishes anything, so that final_state may be the
+        // same buffer
+        if (first >= 0) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) al[r][j] = b[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        s_G[w][lane * VEC + j] = G[j];
+        s_b[w][lane * VEC + j] = b[j];
+    }
+    __syncthreads();
+
+    // 3. one thread per channel: the tile's map out, its entry state in, every
+    // warp's entry state
+    if (threadIdx.x < CT && c0 + threadIdx.x < a.C) {
+        const int ch = threadIdx.x;
+        const bool last_tile = tile == a.tiles - 1;
+        float Gt = 0.f, bt = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            bt = applied(s_G[i][ch], s_b[i][ch], bt);
+            Gt += s_G[i][ch];
+        }
+        float h = 0.f;
+        if (a.ticket) {
+            uint64_t* out = a.words + (size_t)tile * C + c0 + ch;
+            const bool known = tile == 0 || Gt == -INFINITY;
+            if (!last_tile) publish(out, Gt, bt, known);
+            // the entry state is used unless a sequence starts with the tile
+            if (tile > 0 && s_first[0] < 0) {
+                h = look_back(a.words + c0 + ch, C, tile - 1, -1, tile, a.status);
+                if (!known && !last_tile) publish(out, 0.f, applied(Gt, bt, h), true);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const float Gi = s_G[i][ch], bi = s_b[i][ch];
+            s_b[i][ch] = h;
+            h = applied(Gi, bi, h);
+        }
+        if (a.entry) a.entry[(size_t)tile * C + c0 + ch] = s_b[0][ch];
+    }
+    if (!a.h && !a.final_state) return;
+    __syncthreads();
+
+    // 4. the recurrence from this warp's entry state
+    if (!mine) return;
+    float h[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) h[j] = s_b[w][lane * VEC + j];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int t = t0 + w * kR + r;
+        if (t >= a.total) return;
+        const int first = s_first[w * kR + r], last = s_last[w * kR + r];
+        float xv[VEC];
+        xr[r].get(xv);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) h[j] = first >= 0 ? al[r][j] : fmaf(al[r][j], h[j], xv[j]);
+        if (a.h) put(static_cast<T*>(a.h) + (size_t)t * C + c, h);
+        if (last >= 0 && a.final_state) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) a.final_state[(size_t)last * C + c + j] = h[j];
+        }
+    }
+}
+
+template <int VEC, typename T>
+__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanArgs a) {
+    constexpr int CT = 32 * VEC;
+    __shared__ __align__(16) float s_G[kWarps][CT], s_b[kWarps][CT];    // forward maps
+    __shared__ __align__(16) float s_Ge[kWarps][CT], s_e[kWarps][CT];   // maps of e, from the right
+    __shared__ int s_first[kRows], s_last[kRows];
+
+    const int task = next_tile(a), tile = a.tiles - 1 - task / a.ctiles;
+    const int c0 = (task % a.ctiles) * CT;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = c0 + lane * VEC, t0 = tile * kRows;
+    const bool mine = c < a.C;
+    const size_t C = a.C;
+
+    Raw<VEC, T> xr[kR], dr[kR];
+    Raw<VEC, float> gr[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int t = t0 + w * kR + r;
+        xr[r].zero();
+        dr[r].zero();
+        gr[r].zero();
+        if (mine && t < a.total) {
+            xr[r].load(static_cast<const T*>(a.x) + (size_t)t * C + c);
+            gr[r].load(a.g + (size_t)t * C + c);
+            dr[r].load(static_cast<const T*>(a.dout) + (size_t)t * C + c);
+        }
+    }
+    mark_bounds(a, t0, s_first, s_last);
+    if (tile == a.tiles - 1) {
+        if (c0 == 0) report_status(a);
+        pass_empty(a, a.dfinal, a.dh0, c0, min(CT, a.C - c0));
+    }
+
+    // the two maps of this warp's rows
+    float al[kR][VEC];
+    {
+        float G[VEC], b[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const int first = s_first[w * kR + r];
+            float gv[VEC], xv[VEC];
+            gr[r].get(gv);
+            xr[r].get(xv);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                al[r][j] = expf(gv[j]);
+                G[j] = fmaf(gv[j], kLog2e, G[j]);
+            }
+            if (first >= 0) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    G[j] = -INFINITY;
+                    b[j] = a.h0 && mine ? a.h0[(size_t)first * C + c + j] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[r][j], b[j], xv[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            s_G[w][lane * VEC + j] = G[j];
+            s_b[w][lane * VEC + j] = b[j];
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
+#pragma unroll
+        for (int r = kR - 1; r >= 0; --r) {
+            const int last = s_last[w * kR + r];
+            float gv[VEC], dv[VEC];
+            gr[r].get(gv);
+            dr[r].get(dv);
+            if (last >= 0) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    G[j] = -INFINITY;
+                    b[j] = a.dfinal && mine ? a.dfinal[(size_t)last * C + c + j] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                b[j] = al[r][j] * (dv[j] + b[j]);
+                G[j] = fmaf(gv[j], kLog2e, G[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            s_Ge[w][lane * VEC + j] = G[j];
+            s_e[w][lane * VEC + j] = b[j];
+        }
+    }
+    __syncthreads();
+
+    if (threadIdx.x < CT && c0 + threadIdx.x < a.C) {
+        const int ch = threadIdx.x;
+        float Gt = 0.f, bt = 0.f;
+#pragma unroll
+        for (int i = kWarps - 1; i >= 0; --i) {
+            bt = applied(s_Ge[i][ch], s_e[i][ch], bt);
+            Gt += s_Ge[i][ch];
+        }
+        float e = 0.f;
+        if (a.ticket) {
+            uint64_t* out = a.words + (size_t)tile * C + c0 + ch;
+            const bool known = tile == a.tiles - 1 || Gt == -INFINITY;
+            if (tile > 0) publish(out, Gt, bt, known);
+            if (tile < a.tiles - 1 && s_last[kRows - 1] < 0) {
+                e = look_back(a.words + c0 + ch, C, tile + 1, 1, a.tiles - 1 - tile, a.status);
+                if (!known && tile > 0) publish(out, 0.f, applied(Gt, bt, e), true);
+            }
+        }
+#pragma unroll
+        for (int i = kWarps - 1; i >= 0; --i) {
+            const float Gi = s_Ge[i][ch], bi = s_e[i][ch];
+            s_e[i][ch] = e;
+            e = applied(Gi, bi, e);
+        }
+        float h = a.entry[(size_t)tile * C + c0 + ch];
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const float Gi = s_G[i][ch], bi = s_b[i][ch];
+            s_b[i][ch] = h;
+            h = applied(Gi, bi, h);
+        }
+    }
+    __syncthreads();
+
+    if (!mine) return;
+    float hb[kR][VEC], h[VEC], e[VEC];  // hb: the state before each row
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        h[j] = s_b[w][lane * VEC + j];
+        e[j] = s_e[w][lane * VEC + j];
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int first = s_first[w * kR + r];
+        if (first >= 0) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) h[j] = a.h0 ? a.h0[(size_t)first * C + c + j] : 0.f;
+        }
+        float xv[VEC];
+        xr[r].get(xv);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            hb[r][j] = h[j];
+            h[j] = fmaf(al[r][j], h[j], xv[j]);
+        }
+    }
+#pragma unroll
+    for (int r = kR - 1; r >= 0; --r) {
+        const int t = t0 + w * kR + r;
+        if (t >= a.total) continue;
+        const int first = s_first[w * kR + r], last = s_last[w * kR + r];
+        if (last >= 0) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                e[j] = a.dfinal ? a.dfinal[(size_t)last * C + c + j] : 0.f;
+        }
+        float dv[VEC], dgv[VEC];
+        dr[r].get(dv);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            dv[j] += e[j];
+            e[j] = al[r][j] * dv[j];
+            dgv[j] = e[j] * hb[r][j];
+        }
+        put(static_cast<T*>(a.dx) + (size_t)t * C + c, dv);
+        put(a.dg + (size_t)t * C + c, dgv);
+        if (first >= 0 && a.dh0) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) a.dh0[(size_t)first * C + c + j] = e[j];
+        }
+    }
+}
+
+// One token per sequence: state = exp(g) state + x, h = the state in T.
+template <int VEC, typename T>
+__global__ void __launch_bounds__(256) scan_step_kernel(const T* __restrict__ x,
+                                                        const float* __restrict__ g,
+                                                        const float* state_in, float* state_out,
+                                                        T* __restrict__ h, long long n) {
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * VEC;
+    if (i >= n) return;
+    Raw<VEC, T> xr;
+    Raw<VEC, float> gr, sr;
+    xr.load(x + i);
+    gr.load(g + i);
+    sr.load(state_in + i);
+    float xv[VEC], gv[VEC], s[VEC];
+    xr.get(xv);
+    gr.get(gv);
+    sr.get(s);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[j] = fmaf(expf(gv[j]), s[j], xv[j]);
+    put(state_out + i, s);
+    put(h + i, s);
+}
+
+// The workspace of a scan: [0, 256) status word, then the ticket (256 bytes)
+// and one 64-bit word per (tile, channel) -- none of these two when the tokens
+// fit in one tile -- and, for a backward without entry states, those.
+struct ScanSpace {
+    uint32_t* status;
+    uint32_t* ticket;
+    uint64_t* words;
+    float* entry;
+    size_t sync_bytes, total_bytes;
+};
+ScanSpace carve_scan(void* base, int total, int C, bool with_entry) {
+    ScanSpace s{};
+    char* p = static_cast<char*>(base);
+    const size_t tiles = scan_tiles(total);
+    s.status = reinterpret_cast<uint32_t*>(p);
+    size_t off = kAlign;
+    if (tiles > 1) {
+        s.ticket = reinterpret_cast<uint32_t*>(p + off);
+        s.words = reinterpret_cast<uint64_t*>(p + off + kAlign);
+        s.sync_bytes = kAlign + sizeof(uint64_t) * tiles * C;
+        off = align_up(off + s.sync_bytes);
+    }
+    if (with_entry) {
+        s.entry = reinterpret_cast<float*>(p + off);
+        off = align_up(off + sizeof(float) * tiles * C);
+    }
+    s.total_bytes = off;
+    return s;
+}
+
+template <int VEC, typename T>
+cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t st) {
+    a.status = s.status;
+    a.ticket = s.ticket;
+    a.words = s.words;
+    a.tiles = static_cast<int>(scan_tiles(a.total));
+    a.ctiles = (a.C + 32 * VEC - 1) / (32 * VEC);
+    const long long grid = (long long)a.tiles * a.ctiles;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (s.ticket) {
+        const cudaError_t e = cudaMemsetAsync(s.ticket, 0xFF, s.sync_bytes, st);
+        if (e != cudaSuccess) return e;
+    }
+    if (backward)
+        scan_bwd_kernel<VEC, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+    else
+        scan_fwd_kernel<VEC, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, kda_dtype_t dt,
+                          cudaStream_t st) {
+    // rows of C channels start on a 16-byte (fp32) or 8-byte (bf16) boundary
+    // when C is a multiple of 4; other sizes take one channel per lane
+    if (dt == KDA_DTYPE_BF16)
+        return a.C % 4 == 0 ? run_scan<4, __nv_bfloat16>(a, s, backward, st)
+                            : run_scan<1, __nv_bfloat16>(a, s, backward, st);
+    return a.C % 4 == 0 ? run_scan<4, float>(a, s, backward, st)
+                        : run_scan<1, float>(a, s, backward, st);
+}
+
+}  // namespace
+
+size_t scan_workspace_bytes(int total, int C, bool backward) {
+    return carve_scan(nullptr, total, C, backward).total_bytes;
+}
+
+cudaError_t launch_scan_fwd(const void* x, const float* g, const float* h0, const int32_t* cu,
+                            int T, int total, int N, int C, kda_dtype_t dt, void* h,
+                            float* final_state, float* entry, void* workspace, cudaStream_t st) {
+    ScanArgs a{};
+    a.x = x; a.g = g; a.h0 = h0; a.cu = cu; a.T = T; a.total = total; a.N = N; a.C = C;
+    a.h = h; a.final_state = final_state; a.entry = entry;
+    return dispatch_scan(a, carve_scan(workspace, total, C, false), false, dt, st);
+}
+
+cudaError_t launch_scan_bwd(const void* x, const float* g, const float* h0, const void* dout,
+                            const float* dfinal, const float* entry, const int32_t* cu, int T,
+                            int total, int N, int C, kda_dtype_t dt, void* dx, float* dg,
+                            float* dh0, void* workspace, cudaStream_t st) {
+    ScanArgs a{};
+    a.x = x; a.g = g; a.h0 = h0; a.cu = cu; a.T = T; a.total = total; a.N = N; a.C = C;
+    const ScanSpace s = carve_scan(workspace, total, C, entry == nullptr);
+    if (!entry) {
+        a.entry = s.entry;
+        const cudaError_t e = dispatch_scan(a, s, false, dt, st);
+        if (e != cudaSuccess) return e;
+    }
+    a.entry = entry ? const_cast<float*>(entry) : s.entry;
+    a.dout = dout; a.dfinal = dfinal; a.dx = dx; a.dg = dg; a.dh0 = dh0;
+    return dispatch_scan(a, s, true, dt, st);
+}
+
+cudaError_t launch_scan_step(const void* x, const float* g, const float* state_in,
+                             float* state_out, long long n, kda_dtype_t dt, void* h,
+                             cudaStream_t st) {
+    if (n == 0) return cudaSuccess;
+    const bool vec = n % 4 == 0;
+    const unsigned grid = static_cast<unsigned>((n + (vec ? 1023 : 255)) / (vec ? 1024 : 256));
+    if (dt == KDA_DTYPE_BF16) {
+        const __nv_bfloat16* X = static_cast<const __nv_bfloat16*>(x);
+        __nv_bfloat16* Hh = static_cast<__nv_bfloat16*>(h);
+        if (vec)
+            scan_step_kernel<4, __nv_bfloat16><<<grid, 256, 0, st>>>(X, g, state_in, state_out, Hh, n);
+        else
+            scan_step_kernel<1, __nv_bfloat16><<<grid, 256, 0, st>>>(X, g, state_in, state_out, Hh, n);
+    } else {
+        const float* X = static_cast<const float*>(x);
+        float* Hh = static_cast<float*>(h);
+        if (vec)
+            scan_step_kernel<4, float><<<grid, 256, 0, st>>>(X, g, state_in, state_out, Hh, n);
+        else
+            scan_step_kernel<1, float><<<grid, 256, 0, st>>>(X, g, state_in, state_out, Hh, n);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace kda

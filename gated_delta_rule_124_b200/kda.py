@@ -46,6 +46,11 @@ EXPORTS = (
     "kda_chunk_fwd_with_plan", "kda_chunk_fwd_plan_workspace_size",
     "kda_test_overlap_flag_timeout", "kda_layer_decode_step", "kda_layer_chunk_fwd",
     "kda_layer_chunk_fwd_workspace_size", "kda_chunk_state_maps", "kda_fold_segment_states",
+    "kda_linear_scan_num_entries", "kda_linear_scan_workspace_size",
+    "kda_linear_scan_bwd_workspace_size", "kda_linear_scan_fwd", "kda_linear_scan_bwd",
+    "kda_linear_scan_step", "kda_fp8_pitch", "kda_add_rms_norm",
+    "kda_add_rms_norm_bwd_workspace_size", "kda_add_rms_norm_bwd", "kda_quantize_fp8",
+    "kda_fp8_matmul",
 )
 
 
@@ -95,6 +100,18 @@ _SIGS = {
     "kda_chunk_state_maps": ([_vp] * 6 + [_i] * 4 + [_vp, _vp, _vp, _sz, _vp], _i),
     "kda_fold_segment_states": ([_vp] * 3 + [_i] * 6 + [_vp, _vp, _vp], _i),
     "kda_chunk_split_chain": ([_vp] * 3 + [_i] * 4 + [_vp, _vp, _vp, _sz, _vp], _i),
+    "kda_linear_scan_num_entries": ([_i], _i),
+    "kda_linear_scan_workspace_size": ([_i] * 3, _sz),
+    "kda_linear_scan_bwd_workspace_size": ([_i] * 3, _sz),
+    "kda_linear_scan_fwd": ([_vp] * 4 + [_i] * 6 + [_vp] * 4 + [_sz, _vp], _i),
+    "kda_linear_scan_bwd": ([_vp] * 7 + [_i] * 6 + [_vp] * 4 + [_sz, _vp], _i),
+    "kda_linear_scan_step": ([_vp] * 5 + [_i] * 4 + [_vp], _i),
+    "kda_fp8_pitch": ([_i], _i),
+    "kda_add_rms_norm": ([_vp] * 3 + [_i] * 3 + [ctypes.c_float] + [_vp] * 5, _i),
+    "kda_add_rms_norm_bwd_workspace_size": ([_i] * 2, _sz),
+    "kda_add_rms_norm_bwd": ([_vp] * 4 + [_i] * 3 + [ctypes.c_float] + [_vp] * 3 + [_sz, _vp], _i),
+    "kda_quantize_fp8": ([_vp] + [_i] * 5 + [_vp] * 3, _i),
+    "kda_fp8_matmul": ([_vp] * 4 + [_i] * 5 + [_vp] * 2, _i),
 }
 
 # Size of the library's built-in scratch used by kda_chunk_fwd_noalloc.
@@ -138,15 +155,22 @@ def _p(t) -> int | None:
 _TORCH_OF = {KDA_DTYPE_F32: torch.float32, KDA_DTYPE_BF16: torch.bfloat16}
 
 
-def _check(what, dtype=None, typed=(), f32=(), i32=(), raw=()):
+_FP8_BYTES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _check(what, dtype=None, typed=(), f32=(), i32=(), raw=(), f8=()):
     """Reject tensors the C ABI would misread, before any pointer is passed:
     every tensor must be contiguous and on one device; `typed` tensors (q, k,
     v, o, dout ...) must have the call's dtype, `f32` ones (g, beta, states,
-    gradients) float32, `i32` ones (cu_seqlens) int32; `raw` ones (workspaces)
-    only contiguous.  Plain ints (raw addresses) and None are not checked."""
+    gradients) float32, `i32` ones (cu_seqlens) int32, `f8` ones (e4m3 codes)
+    float8_e4m3fn or uint8; `raw` ones (workspaces) only contiguous.  Plain ints (raw addresses) and None are not checked."""
     want = None if dtype is None else _TORCH_OF[dtype_code(dtype)]
     dev = None
-    for group, need in ((typed, want), (f32, torch.float32), (i32, torch.int32), (raw, None)):
+    for t in f8:
+        if isinstance(t, torch.Tensor) and t.dtype not in _FP8_BYTES:
+            raise ValueError(f"{what}: expected float8_e4m3fn or uint8, got {t.dtype}")
+    for group, need in ((typed, want), (f32, torch.float32), (i32, torch.int32), (raw, None),
+                        (f8, None)):
         for t in group:
             if t is None or isinstance(t, int):
                 continue
@@ -171,6 +195,30 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _enqueue(name, tensor, stream, check, *args) -> int:
+    """The library's call `name` with `args` and the stream: the given one, or
+    the current stream of `tensor`'s device, which is the current device during
+    the call."""
+    fn = getattr(load(), name)
+    dev = tensor.device if isinstance(tensor, torch.Tensor) else None
+    if dev is None or dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        return _ret(fn(*args, _stream(stream)), name, check)
+    with torch.cuda.device(dev):
+        return _ret(fn(*args, _stream(stream)), name, check)
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors allocated here for work on a stream of the caller's: their memory
+    is not reused before that work is done."""
+    if stream is None:
+        return
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            s = (torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int)
+                 else stream)
+            t.record_stream(s)
 
 
 def dtype_code(dtype) -> int:
@@ -492,6 +540,86 @@ def kda_decode_step(q, k, v, g, beta, state, o, N, H, dk, dv, dtype, stream=None
     return _ret(st, "kda_decode_step", check)
 
 
+def kda_linear_scan_num_entries(total_tokens) -> int:
+    return int(load().kda_linear_scan_num_entries(total_tokens))
+
+
+def kda_linear_scan_workspace_size(total_tokens, H, d) -> int:
+    return int(load().kda_linear_scan_workspace_size(total_tokens, H, d))
+
+
+def kda_linear_scan_bwd_workspace_size(total_tokens, H, d) -> int:
+    return int(load().kda_linear_scan_bwd_workspace_size(total_tokens, H, d))
+
+
+def kda_linear_scan_fwd(x, g, initial_state, cu_seqlens, B, T, num_seqs, H, d, dtype, h,
+                        final_state, entry_states, workspace, workspace_bytes=None, stream=None,
+                        check=True) -> int:
+    _check("kda_linear_scan_fwd", dtype, typed=(x, h),
+           f32=(g, initial_state, final_state, entry_states), i32=(cu_seqlens,), raw=(workspace,))
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    return _enqueue("kda_linear_scan_fwd", x, stream, check, _p(x), _p(g), _p(initial_state),
+                    _p(cu_seqlens), B, T, num_seqs, H, d, dtype_code(dtype), _p(h),
+                    _p(final_state), _p(entry_states), _p(workspace), wb)
+
+
+def kda_linear_scan_bwd(x, g, initial_state, dout, dfinal_state, entry_states, cu_seqlens, B, T,
+                        num_seqs, H, d, dtype, dx, dg, dinitial_state, workspace,
+                        workspace_bytes=None, stream=None, check=True) -> int:
+    _check("kda_linear_scan_bwd", dtype, typed=(x, dout, dx),
+           f32=(g, initial_state, dfinal_state, entry_states, dg, dinitial_state),
+           i32=(cu_seqlens,), raw=(workspace,))
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    return _enqueue("kda_linear_scan_bwd", x, stream, check, _p(x), _p(g), _p(initial_state),
+                    _p(dout), _p(dfinal_state), _p(entry_states), _p(cu_seqlens), B, T, num_seqs,
+                    H, d, dtype_code(dtype), _p(dx), _p(dg), _p(dinitial_state), _p(workspace),
+                    wb)
+
+
+def kda_linear_scan_step(x, g, state_in, state_out, h, N, H, d, dtype, stream=None,
+                         check=True) -> int:
+    _check("kda_linear_scan_step", dtype, typed=(x, h), f32=(g, state_in, state_out))
+    return _enqueue("kda_linear_scan_step", x, stream, check, _p(x), _p(g), _p(state_in),
+                    _p(state_out), _p(h), N, H, d, dtype_code(dtype))
+
+
+def kda_fp8_pitch(K) -> int:
+    return int(load().kda_fp8_pitch(K))
+
+
+def kda_add_rms_norm(x, residual, w, rows, D, dtype, eps, sum, y, y8, y8_scale, stream=None,
+                     check=True) -> int:
+    _check("kda_add_rms_norm", dtype, typed=(x, residual, sum, y), f32=(w, y8_scale), f8=(y8,))
+    return _enqueue("kda_add_rms_norm", x, stream, check, _p(x), _p(residual), _p(w), rows, D,
+                    dtype_code(dtype), float(eps), _p(sum), _p(y), _p(y8), _p(y8_scale))
+
+
+def kda_add_rms_norm_bwd_workspace_size(rows, D) -> int:
+    return int(load().kda_add_rms_norm_bwd_workspace_size(rows, D))
+
+
+def kda_add_rms_norm_bwd(s, w, dy, dsum, rows, D, dtype, eps, dx, dw, workspace,
+                         workspace_bytes=None, stream=None, check=True) -> int:
+    _check("kda_add_rms_norm_bwd", dtype, typed=(s, dy, dsum, dx), f32=(w, dw), raw=(workspace,))
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    return _enqueue("kda_add_rms_norm_bwd", s, stream, check, _p(s), _p(w), _p(dy), _p(dsum),
+                    rows, D, dtype_code(dtype), float(eps), _p(dx), _p(dw), _p(workspace), wb)
+
+
+def kda_quantize_fp8(x, rows, cols, dtype, block_rows, transpose, y8, scale, stream=None,
+                     check=True) -> int:
+    _check("kda_quantize_fp8", dtype, typed=(x,), f32=(scale,), f8=(y8,))
+    return _enqueue("kda_quantize_fp8", x, stream, check, _p(x), rows, cols, dtype_code(dtype),
+                    block_rows, int(bool(transpose)), _p(y8), _p(scale))
+
+
+def kda_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, out, stream=None,
+                   check=True) -> int:
+    _check("kda_fp8_matmul", out_dtype, typed=(out,), f32=(a_scale, b_scale), f8=(a8, b8))
+    return _enqueue("kda_fp8_matmul", a8, stream, check, _p(a8), _p(a_scale), _p(b8), _p(b_scale),
+                    M, N, K, b_block_rows, dtype_code(out_dtype), _p(out))
+
+
 def kda_chunk_fwd_noalloc(q, k, v, g, beta, initial_state, cu_seqlens, B, T, num_seqs, H, dk,
                           dv, chunk, dtype, o, final_state, stream=None, check=True) -> int:
     """kda_chunk_fwd without a workspace: for callers that may not allocate
@@ -633,3 +761,262 @@ def decode_step(q, k, v, g, beta, state, o=None, stream=None):
         o = torch.empty(N, H, dv, dtype=v.dtype, device=v.device)
     kda_decode_step(q, k, v, g, beta, state, o, N, H, dk, dv, q.dtype, stream=stream)
     return o
+
+
+# ----------------------------------------------------- gated linear recurrence
+
+def _scan_shape(what, x, cu_seqlens):
+    """(B, T, N, H, d) of x [B, T, H, d] or [T_total, H, d]."""
+    if x.dim() == 3:
+        total, H, d = x.shape
+        return 1, total, 1 if cu_seqlens is None else cu_seqlens.numel() - 1, H, d
+    if x.dim() != 4:
+        raise ValueError(f"{what}: x is [B, T, H, d] or [T_total, H, d], got {tuple(x.shape)}")
+    if cu_seqlens is not None:
+        raise ValueError(f"{what}: cu_seqlens needs packed [T_total, H, d] inputs")
+    B, T, H, d = x.shape
+    return B, T, B, H, d
+
+
+def _same_shape(what, shape, **tensors):
+    for name, t in tensors.items():
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: {name} is {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def linear_scan(x, g, initial_state=None, cu_seqlens=None, output_final_state=True,
+                output_entry_states=False, workspace=None, stream=None):
+    """Gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t per channel.  x [B, T,
+    H, d] or [T_total, H, d] (packed with cu_seqlens), bf16 or fp32; g like x,
+    fp32; initial_state [N, H, d] fp32.  Returns (h, final_state or None), and
+    the entry states linear_scan_bwd takes if output_entry_states."""
+    B, T, N, H, d = _scan_shape("linear_scan", x, cu_seqlens)
+    _same_shape("linear_scan", x.shape, g=g)
+    _same_shape("linear_scan", (N, H, d), initial_state=initial_state)
+    total, f32 = B * T, dict(dtype=torch.float32, device=x.device)
+    h = torch.empty_like(x)
+    hN = torch.empty(N, H, d, **f32) if output_final_state else None
+    entry = (torch.empty(kda_linear_scan_num_entries(total), H, d, **f32)
+             if output_entry_states else None)
+    if workspace is None:
+        workspace = torch.empty(kda_linear_scan_workspace_size(total, H, d), dtype=torch.uint8,
+                                device=x.device)
+    kda_linear_scan_fwd(x, g, initial_state, cu_seqlens, B, T, N, H, d, x.dtype, h, hN, entry,
+                        workspace, stream=stream)
+    _used_on(stream, h, hN, entry, workspace)
+    return (h, hN, entry) if output_entry_states else (h, hN)
+
+
+def linear_scan_bwd(x, g, dout, initial_state=None, dfinal_state=None, cu_seqlens=None,
+                    entry_states=None, workspace=None, stream=None):
+    """Gradients of sum(h * dout) + sum(final_state * dfinal_state) for
+    linear_scan's inputs: (dx like x, dg fp32, dinitial_state [N, H, d] fp32)."""
+    B, T, N, H, d = _scan_shape("linear_scan_bwd", x, cu_seqlens)
+    total, f32 = B * T, dict(dtype=torch.float32, device=x.device)
+    _same_shape("linear_scan_bwd", x.shape, g=g, dout=dout)
+    _same_shape("linear_scan_bwd", (N, H, d), initial_state=initial_state,
+                dfinal_state=dfinal_state)
+    if entry_states is not None:
+        _same_shape("linear_scan_bwd", (kda_linear_scan_num_entries(total), H, d),
+                    entry_states=entry_states)
+    dx, dg = torch.empty_like(x), torch.empty(x.shape, **f32)
+    dh0 = torch.empty(N, H, d, **f32)
+    if workspace is None:
+        workspace = torch.empty(kda_linear_scan_bwd_workspace_size(total, H, d),
+                                dtype=torch.uint8, device=x.device)
+    kda_linear_scan_bwd(x, g, initial_state, dout, dfinal_state, entry_states, cu_seqlens, B, T,
+                        N, H, d, x.dtype, dx, dg, dh0, workspace, stream=stream)
+    _used_on(stream, dx, dg, dh0, workspace)
+    return dx, dg, dh0
+
+
+class LinearScan(torch.autograd.Function):
+    """Differentiable linear_scan; keeps its inputs and one state per 64 tokens."""
+
+    @staticmethod
+    def forward(ctx, x, g, initial_state, cu_seqlens):
+        ctx.set_materialize_grads(False)
+        h, hN, entry = linear_scan(x, g, initial_state, cu_seqlens=cu_seqlens,
+                                   output_entry_states=True)
+        ctx.save_for_backward(x, g, initial_state, cu_seqlens, entry)
+        return h, hN
+
+    @staticmethod
+    def backward(ctx, dh, dhN):
+        x, g, h0, cu, entry = ctx.saved_tensors
+        dh = torch.zeros_like(x) if dh is None else dh.to(x.dtype).contiguous()
+        dhN = None if dhN is None else dhN.float().contiguous()
+        dx, dg, dh0 = linear_scan_bwd(x, g, dh, h0, dhN, cu_seqlens=cu, entry_states=entry)
+        return dx, dg, dh0 if h0 is not None else None, None
+
+
+def gated_linear_scan(x, g, initial_state=None, cu_seqlens=None):
+    """Differentiable gated linear recurrence: (h, final_state); see LinearScan."""
+    return LinearScan.apply(x, g, initial_state, cu_seqlens)
+
+
+def linear_scan_step(x, g, state, h=None, state_out=None, stream=None):
+    """One token of the recurrence.  x, g [N, H, d]; state [N, H, d] fp32, updated
+    in place (or left alone, with the new one in state_out).  Returns h."""
+    N, H, d = x.shape
+    _same_shape("linear_scan_step", x.shape, g=g, state=state, h=h, state_out=state_out)
+    made = h is None
+    if made:
+        h = torch.empty_like(x)
+    kda_linear_scan_step(x, g, state, state if state_out is None else state_out, h, N, H, d,
+                         x.dtype, stream=stream)
+    if made:
+        _used_on(stream, h)
+    return h
+
+
+# ----------------------------------- pre-norm, 8-bit matrices and their product
+
+def _blocks128(n) -> int:
+    return (n + 127) // 128
+
+
+def add_rms_norm(x, w, residual=None, eps=1e-6, quantize=False, sum=None, stream=None):
+    """RMS norm of s = x + residual over the last dimension, times w (fp32).
+    Returns (s, y), or with quantize=True (s, y8, scale): y as an 8-bit matrix
+    (see quantize_fp8).  s is x itself without a residual; `sum` may be given for
+    it (x or residual, to update it in place)."""
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    _same_shape("add_rms_norm", x.shape, residual=residual, sum=sum)
+    _same_shape("add_rms_norm", (D,), w=w)
+    s = sum
+    if s is None:
+        s = x if residual is None else torch.empty_like(x)
+    y = y8 = scale = None
+    if quantize:
+        y8 = torch.empty(rows, kda_fp8_pitch(D), dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty(_blocks128(D), rows, dtype=torch.float32, device=x.device)
+    else:
+        y = torch.empty_like(x)
+    kda_add_rms_norm(x, residual, w, rows, D, x.dtype, eps, None if s is x else s, y, y8, scale,
+                     stream=stream)
+    _used_on(stream, s, y, y8, scale)
+    return (s, y8, scale) if quantize else (s, y)
+
+
+def add_rms_norm_bwd(s, w, dy, dsum=None, eps=1e-6, workspace=None, stream=None):
+    """Gradients of sum(y * dy) + sum(s * dsum) for add_rms_norm: (dx, dw); dx is
+    the gradient of x and of the residual."""
+    D = s.shape[-1]
+    rows = s.numel() // D if D else 0
+    _same_shape("add_rms_norm_bwd", s.shape, dy=dy, dsum=dsum)
+    _same_shape("add_rms_norm_bwd", (D,), w=w)
+    dx, dw = torch.empty_like(s), torch.empty_like(w)
+    if workspace is None:
+        workspace = torch.empty(kda_add_rms_norm_bwd_workspace_size(rows, D), dtype=torch.uint8,
+                                device=s.device)
+    kda_add_rms_norm_bwd(s, w, dy, dsum, rows, D, s.dtype, eps, dx, dw, workspace, stream=stream)
+    _used_on(stream, dx, dw, workspace)
+    return dx, dw
+
+
+class AddRMSNorm(torch.autograd.Function):
+    """Differentiable add_rms_norm: (s, y)."""
+
+    @staticmethod
+    def forward(ctx, x, w, residual, eps):
+        ctx.set_materialize_grads(False)
+        s, y = add_rms_norm(x, w, residual, eps=eps)
+        ctx.eps, ctx.has_residual = eps, residual is not None
+        ctx.save_for_backward(s, w)
+        return (s, y) if residual is not None else (s.view_as(s), y)
+
+    @staticmethod
+    def backward(ctx, ds, dy):
+        s, w = ctx.saved_tensors
+        if dy is None:
+            return ds, None, ds if ctx.has_residual else None, None
+        ds = None if ds is None else ds.to(s.dtype).contiguous()
+        dx, dw = add_rms_norm_bwd(s, w, dy.to(s.dtype).contiguous(), ds, eps=ctx.eps)
+        return dx, dw, dx if ctx.has_residual else None, None
+
+
+def residual_rms_norm(x, w, residual=None, eps=1e-6):
+    """Differentiable residual addition and RMS norm: (x + residual, y)."""
+    return AddRMSNorm.apply(x, w, residual, eps)
+
+
+def quantize_fp8(x, block_rows=1, transpose=False, stream=None):
+    """x [rows, cols] (bf16 or fp32) as an 8-bit matrix [R, K], x or its transpose:
+    (y8, scale) with y8 [R, K rounded up to 16] float8_e4m3fn and scale [ceil(K /
+    128), R] fp32, or [ceil(K / 128), ceil(R / 128)] with block_rows=128."""
+    if x.dim() != 2:
+        raise ValueError(f"quantize_fp8: x is [rows, cols], got {tuple(x.shape)}")
+    rows, cols = x.shape
+    R, K = (cols, rows) if transpose else (rows, cols)
+    y8 = torch.empty(R, kda_fp8_pitch(K), dtype=torch.float8_e4m3fn, device=x.device)
+    scale = torch.empty(_blocks128(K), R if block_rows == 1 else _blocks128(R),
+                        dtype=torch.float32, device=x.device)
+    kda_quantize_fp8(x, rows, cols, x.dtype, block_rows, transpose, y8, scale, stream=stream)
+    _used_on(stream, y8, scale)
+    return y8, scale
+
+
+def fp8_matmul(a8, a_scale, b8, b_scale, K=None, b_block_rows=128, out_dtype=torch.bfloat16,
+               out=None, stream=None):
+    """out [M, N] = a b^T of two 8-bit matrices as quantize_fp8 makes them, a with a
+    scale per row, b per row (b_block_rows=1) or per 128 rows.  K: the number of
+    columns that count, where the rows are padded."""
+    M, N = a8.shape[0], b8.shape[0]
+    if K is None:
+        K = a8.shape[1]
+    pitch = kda_fp8_pitch(K)
+    _same_shape("fp8_matmul", (M, pitch), a8=a8)
+    _same_shape("fp8_matmul", (N, pitch), b8=b8)
+    _same_shape("fp8_matmul", (_blocks128(K), M), a_scale=a_scale)
+    _same_shape("fp8_matmul", (_blocks128(K), N if b_block_rows == 1 else _blocks128(N)),
+                b_scale=b_scale)
+    made = out is None
+    if made:
+        out = torch.empty(M, N, dtype=out_dtype, device=a8.device)
+    _same_shape("fp8_matmul", (M, N), out=out)
+    kda_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out.dtype, out, stream=stream)
+    if made:
+        _used_on(stream, out)
+    return out
+
+
+class Fp8Linear(torch.autograd.Function):
+    """y = x w^T with both operands in 8 bits, forward and backward: x and the
+    gradient of y with a scale per row and 128 columns (per column and 128 tokens
+    for the weight's gradient), w with one per 128 x 128 block."""
+
+    @staticmethod
+    def forward(ctx, x, w):
+        x2 = x.reshape(-1, x.shape[-1]).contiguous()
+        w8, w_scale = quantize_fp8(w, block_rows=128)
+        x8, x_scale = quantize_fp8(x2)
+        ctx.save_for_backward(x2, w)
+        ctx.shape = x.shape
+        y = fp8_matmul(x8, x_scale, w8, w_scale, K=w.shape[1], out_dtype=x.dtype)
+        return y.view(*x.shape[:-1], w.shape[0])
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, w = ctx.saved_tensors
+        (M, K), N = x2.shape, w.shape[0]
+        dy2 = dy.reshape(M, N).to(x2.dtype).contiguous()
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            d8, d_scale = quantize_fp8(dy2)
+            wt8, wt_scale = quantize_fp8(w, block_rows=128, transpose=True)
+            dx = fp8_matmul(d8, d_scale, wt8, wt_scale, K=N, out_dtype=x2.dtype).view(ctx.shape)
+        if ctx.needs_input_grad[1]:
+            if M == 0:
+                return dx, torch.zeros_like(w)
+            d8, d_scale = quantize_fp8(dy2, transpose=True)
+            x8, x_scale = quantize_fp8(x2, transpose=True)
+            dw = fp8_matmul(d8, d_scale, x8, x_scale, K=M, b_block_rows=1, out_dtype=w.dtype)
+        return dx, dw
+
+
+def fp8_linear(x, w):
+    """Differentiable projection x [..., in] (bf16 or fp32) by w [out, in] with 8-bit
+    operands; see Fp8Linear."""
+    return Fp8Linear.apply(x, w)

@@ -497,6 +497,134 @@ kda_status_t kda_layer_decode_step(const void* xq, const void* xk, const void* x
                                   kda_dtype_t dtype, float l2_eps, float rms_eps, void* y,
                                   void* stream);
 
+/* -------------------------------------------- gated linear recurrence
+ * The recurrence of the operator without its key side, one state value per
+ * channel (Kimi Linear (aiwiki.ai), "Background: from the delta rule to gated
+ * DeltaNet", the gated linear recurrences the delta rule extends):
+ *     h_t = exp(g_t) h_{t-1} + x_t        per (sequence, head, channel).
+ *
+ * kda_linear_scan_fwd
+ * In:  x [total, H, d] (dtype); g [total, H, d] fp32; initial_state [num_seqs,
+ *      H, d] fp32 or NULL (zeros); cu_seqlens / B / T / num_seqs as for
+ *      kda_chunk_fwd.  g is any finite value.
+ * Out: h [total, H, d] (dtype), not aliasing the inputs; final_state [num_seqs,
+ *      H, d] fp32 or NULL (not written), which may be initial_state;
+ *      entry_states [kda_linear_scan_num_entries(total), H, d] fp32 or NULL:
+ *      the state before every 64th token, which kda_linear_scan_bwd takes.
+ * An empty sequence passes its initial state on.  The state is fp32 throughout
+ * and h one rounding of it; a NaN or an infinity stays inside its channel and
+ * sequence.  One pass over x and g whatever the lengths: long sequences are
+ * split over time, and results do not depend on the order of execution beyond
+ * the rounding of states at the split (the tiles compose in one order, but
+ * from the maps or from an exit state, whichever is there).
+ * Workspace: kda_linear_scan_workspace_size(total, H, d) bytes, 256-byte
+ *      aligned, starting with the status word of kda_get_device_status
+ *      (KDA_ERR_BAD_SEQLENS, KDA_ERR_TIMEOUT: outputs unspecified).  Calls
+ *      whose work may overlap need workspaces of their own.
+ * Shapes: H >= 1, d >= 1, H d <= 2^24 (multiples of 4 run four channels a lane).
+ *
+ * kda_linear_scan_bwd: gradients of sum(h * dout) + sum(final_state *
+ * dfinal_state).
+ * In:  x, g, initial_state, the sequence arguments as in the forward; dout
+ *      [total, H, d] (dtype); dfinal_state [num_seqs, H, d] fp32 or NULL
+ *      (zeros); entry_states as the forward wrote them, or NULL (they are
+ *      recomputed, one more pass over x and g).
+ * Out: dx [total, H, d] (dtype, one rounding), dg [total, H, d] fp32,
+ *      dinitial_state [num_seqs, H, d] fp32 or NULL (not written); none aliases
+ *      an input.  Workspace: kda_linear_scan_bwd_workspace_size().
+ *
+ * kda_linear_scan_step: one token for each of N sequences, state_out = exp(g)
+ * state_in + x and h = state_out in dtype.  x, h [N, H, d] (dtype), g [N, H, d]
+ * fp32, states [N, H, d] fp32; state_out may be state_in.  No workspace; N = 0
+ * does nothing.
+ */
+int kda_linear_scan_num_entries(int total_tokens);
+size_t kda_linear_scan_workspace_size(int total_tokens, int H, int d);
+size_t kda_linear_scan_bwd_workspace_size(int total_tokens, int H, int d);
+
+kda_status_t kda_linear_scan_fwd(const void* x, const float* g, const float* initial_state,
+                                 const int32_t* cu_seqlens, int B, int T, int num_seqs, int H,
+                                 int d, kda_dtype_t dtype, void* h, float* final_state,
+                                 float* entry_states, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+kda_status_t kda_linear_scan_bwd(const void* x, const float* g, const float* initial_state,
+                                 const void* dout, const float* dfinal_state,
+                                 const float* entry_states, const int32_t* cu_seqlens, int B,
+                                 int T, int num_seqs, int H, int d, kda_dtype_t dtype, void* dx,
+                                 float* dg, float* dinitial_state, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+kda_status_t kda_linear_scan_step(const void* x, const float* g, const float* state_in,
+                                  float* state_out, void* h, int N, int H, int d,
+                                  kda_dtype_t dtype, void* stream);
+
+/* ------------------------------------- pre-norm, 8-bit matrices, projections
+ * What surrounds the layer's core: the RMS norm before it with the residual's
+ * addition, and the projections to q, k, v, gates and back as products of 8-bit
+ * matrices.
+ *
+ * An 8-bit matrix [R, K] holds e4m3 codes, one byte each, in rows of
+ * kda_fp8_pitch(K) bytes (K rounded up to 16; bytes beyond K are written as
+ * zeros and not read as values).  Its scales are fp32, for blocks of 128
+ * columns of one row ([ceil(K / 128), R]) or of 128 rows ([ceil(K / 128),
+ * ceil(R / 128)]); element (r, k) stands for code * scale of its block.  The
+ * quantising calls take scale = amax / 448, amax the block's largest magnitude
+ * (at least 2^-100), and round code = x * (448 / amax) to nearest.  A NaN
+ * stays a NaN and leaves its block's scale alone; a block that holds an
+ * infinity stands for NaN.
+ *
+ * kda_add_rms_norm: s = x + residual (residual NULL: s = x), rounded to dtype;
+ *   y = s / sqrt(mean(s^2) + eps) * w over each row of D.
+ * In:  x, residual [rows, D] (dtype); w [D] fp32; eps > 0.
+ * Out: sum [rows, D] (dtype) or NULL: s; y [rows, D] (dtype) or NULL; y8
+ *      [rows, kda_fp8_pitch(D)] and y8_scale [ceil(D / 128), rows] fp32, both
+ *      or neither; at least one of y and y8.  sum may be x or residual.
+ * Shapes: D a multiple of 8, 8 <= D <= 16384.  rows = 0 does nothing.
+ *
+ * kda_add_rms_norm_bwd: gradients of sum(y * dy) + sum(sum * dsum).
+ * In:  s [rows, D]: sum as the forward wrote it (or x without a residual); w;
+ *      dy [rows, D] (dtype); dsum [rows, D] (dtype) or NULL (zeros).
+ * Out: dx [rows, D] (dtype, one rounding): the gradient of x and of residual;
+ *      it may be dsum, but not s or dy; dw [D] fp32, summed in a fixed order.
+ * Workspace: kda_add_rms_norm_bwd_workspace_size(rows, D) bytes, 256-byte
+ *      aligned.  The 8-bit output has the gradient of y.
+ *
+ * kda_quantize_fp8: x [rows, cols] (dtype) as an 8-bit matrix, block_rows 1 or
+ *   128; transpose != 0: the 8-bit matrix of x^T (R = cols, K = rows).
+ * Out: y8 [R, kda_fp8_pitch(K)], scale as above.  Any rows >= 0, cols >= 1.
+ *
+ * kda_fp8_matmul: out[m, n] = sum_k a[m, k] b[n, k] of two 8-bit matrices, a
+ *   [M, K] with a scale per row and block, b [N, K] with a scale per row
+ *   (b_block_rows = 1) or per 128 rows (128).  The products inside a block of
+ *   128 are added up on the tensor cores in fp32, the blocks in fp32; out
+ *   [M, N] in out_dtype, one rounding.  With b a weight [out, in] it is the
+ *   projection of a; with b the transposed weight the gradient of a
+ *   projection's input; with both operands transposed (K: tokens,
+ *   b_block_rows 1) the gradient of its weight.  Any M >= 0, N >= 1, K >= 1.
+ *   No workspace.  KDA_ERR_UNSUPPORTED without a driver that makes tensor maps.
+ */
+int kda_fp8_pitch(int K);
+
+kda_status_t kda_add_rms_norm(const void* x, const void* residual, const float* w, int rows,
+                              int D, kda_dtype_t dtype, float eps, void* sum, void* y, void* y8,
+                              float* y8_scale, void* stream);
+
+size_t kda_add_rms_norm_bwd_workspace_size(int rows, int D);
+
+kda_status_t kda_add_rms_norm_bwd(const void* s, const float* w, const void* dy, const void* dsum,
+                                  int rows, int D, kda_dtype_t dtype, float eps, void* dx,
+                                  float* dw, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+kda_status_t kda_quantize_fp8(const void* x, int rows, int cols, kda_dtype_t dtype,
+                              int block_rows, int transpose, void* y8, float* scale,
+                              void* stream);
+
+kda_status_t kda_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
+                            const float* b_scale, int M, int N, int K, int b_block_rows,
+                            kda_dtype_t out_dtype, void* out, void* stream);
+
 /* ------------------------------------------------ prefill, no allocation
  * kda_chunk_fwd_noalloc: the same computation as kda_chunk_fwd, with no
  * workspace argument, for callers that may not obtain device memory: an
