@@ -4,23 +4,103 @@
 //
 // Elements are read once and written once as one byte: bound by HBM.  A CTA of
 // 256 threads takes a 128 x 128 tile of x, a row's 128 columns in 16 lanes,
-// eight rows a thread, all loads issued at once; a block's maximum is a
-// shuffle over those lanes, and over the CTA for a 128 x 128 block.  For the
-// transpose the tile goes through shared memory, where a thread takes two
-// neighbouring columns of 32 rows, so that it reads whole words without bank
-// conflicts and writes whole 32-byte sectors of two rows of the result.
+// eight rows a thread, all loads issued at once and kept as they came (bf16
+// pairs), so that several CTAs fit on an SM; a block's maximum is a shuffle
+// over those lanes, and over the CTA for a 128 x 128 block.  For the transpose
+// the tile goes to shared memory by asynchronous copies, and a thread takes two
+// neighbouring columns of 32 rows from there, so that it reads whole words
+// without bank conflicts and writes whole 32-byte sectors of two rows of the
+// result.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "kda_common.cuh"
 #include "kda_fp8.cuh"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 8;  // vectors of eight elements: rows ty, ty + 16, ...
+
+// Two neighbouring elements and what is done with them.
+template <typename T>
+struct Two;
+template <>
+struct Two<__nv_bfloat16> {
+    uint32_t v;
+    __device__ float lo() const { return __uint_as_float(v << 16); }
+    __device__ float hi() const { return __uint_as_float(v & 0xFFFF0000u); }
+};
+template <>
+struct Two<float> {
+    float2 v;
+    __device__ float lo() const { return v.x; }
+    __device__ float hi() const { return v.y; }
+};
+// Running maxima of the magnitudes of both (a NaN is passed over).
+__device__ __forceinline__ void max_abs(float2& m, Two<__nv_bfloat16> x) {
+    m.x = fmaxf(m.x, fabsf(x.lo()));
+    m.y = fmaxf(m.y, fabsf(x.hi()));
+}
+__device__ __forceinline__ void max_abs(float2& m, Two<float> x) {
+    m.x = fmaxf(m.x, fabsf(x.v.x));
+    m.y = fmaxf(m.y, fabsf(x.v.y));
+}
+
+// Eight elements of a row as they lie in memory.
+template <typename T>
+struct Row8 {
+    Two<T> p[4];
+    __device__ float max_abs8() const {
+        float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) max_abs(m, p[i]);
+        return fmaxf(m.x, m.y);
+    }
+    __device__ uint2 codes(float f) const {
+        return make_uint2(
+            fp8x4(p[0].lo() * f, p[0].hi() * f, p[1].lo() * f, p[1].hi() * f),
+            fp8x4(p[2].lo() * f, p[2].hi() * f, p[3].lo() * f, p[3].hi() * f));
+    }
+};
+__device__ __forceinline__ void load(Row8<__nv_bfloat16>& r, const __nv_bfloat16* p) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    r.p[0].v = u.x; r.p[1].v = u.y; r.p[2].v = u.z; r.p[3].v = u.w;
+}
+__device__ __forceinline__ void load(Row8<float>& r, const float* p) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    r.p[0].v = make_float2(a.x, a.y); r.p[1].v = make_float2(a.z, a.w);
+    r.p[2].v = make_float2(b.x, b.y); r.p[3].v = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ void set(Row8<__nv_bfloat16>& r, const __nv_bfloat16 (&e)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r.p[i].v = static_cast<uint32_t>(__bfloat16_as_ushort(e[2 * i + 1])) << 16 |
+                   __bfloat16_as_ushort(e[2 * i]);
+}
+__device__ __forceinline__ void set(Row8<float>& r, const float (&e)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i].v = make_float2(e[2 * i], e[2 * i + 1]);
+}
+
+// Elements [c, c + 8) of row r, zeros outside the matrix.
+template <typename T>
+__device__ __forceinline__ Row8<T> row8(const T* x, int rows, int cols, bool vec, int r, int c) {
+    Row8<T> v;
+    const T* p = x + (size_t)r * cols + c;
+    if (vec && r < rows && c < cols) {
+        load(v, p);
+    } else {
+        T e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = r < rows && c + j < cols ? p[j] : from_f32<T>(0.f);
+        set(v, e);
+    }
+    return v;
+}
 
 __device__ __forceinline__ float cta_max(float m, float* buf) {
 #pragma unroll
@@ -33,155 +113,150 @@ __device__ __forceinline__ float cta_max(float m, float* buf) {
     return m;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_row8(const T* x, int rows, int cols, bool vec, int r, int c,
-                                          float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    if (r >= rows || c >= cols) return;
-    const T* p = x + (size_t)r * cols + c;
-    if (vec) {
-        load_vec8(p, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < cols) v[j] = to_f32(p[j]);
-    }
-}
-
-template <typename T, bool kRowBlocks>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, int rows,
-                                                            int cols, int pitch, bool vec,
-                                                            uint8_t* __restrict__ y8,
-                                                            float* __restrict__ scale) {
+template <typename T, bool kRowBlocks, bool kVec>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    quantize_kernel(const T* __restrict__ x, int rows, int cols, int pitch,
+                    uint8_t* __restrict__ y8, float* __restrict__ scale) {
     __shared__ float s_max[kThreads / 32];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int KB = (cols + 127) / 128, RB = (rows + 127) / 128;
     const int kb = blockIdx.x % KB, rb = blockIdx.x / KB, c = kb * 128 + tx * 8;
-    float v[kPerThread][8];
+    Row8<T> v[8];
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-        load_row8(x, rows, cols, vec, rb * 128 + ty + 16 * i, c, v[i]);
+    for (int i = 0; i < 8; ++i) v[i] = row8(x, rows, cols, kVec, rb * 128 + ty + 16 * i, c);
     float amax = 0.f;
     if (!kRowBlocks) {
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) amax = fmaxf(amax, max_abs8(v[i]));
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, v[i].max_abs8());
         amax = cta_max(amax, s_max);
         if (threadIdx.x == 0) scale[(size_t)kb * RB + rb] = fp8_scale(amax);
     }
+    float f = fp8_factor(amax);
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const int r = rb * 128 + ty + 16 * i;
         if (kRowBlocks) {
-            amax = max16(max_abs8(v[i]));
+            amax = max16(v[i].max_abs8());
+            f = fp8_factor(amax);
             if (tx == 0 && r < rows) scale[(size_t)kb * rows + r] = fp8_scale(amax);
         }
         if (r < rows && c < pitch)
-            *reinterpret_cast<uint2*>(y8 + (size_t)r * pitch + c) = quantize8(v[i], fp8_factor(amax));
+            *reinterpret_cast<uint2*>(y8 + (size_t)r * pitch + c) = v[i].codes(f);
     }
 }
 
 // x [rows, cols] -> y8 [cols, pitch], pitch >= rows; blocks along x's rows.
-template <typename T, bool kRowBlocks>
-__global__ void __launch_bounds__(kThreads) quantize_t_kernel(const T* __restrict__ x, int rows,
-                                                              int cols, int pitch, bool vec,
-                                                              uint8_t* __restrict__ y8,
-                                                              float* __restrict__ scale) {
+template <typename T, bool kRowBlocks, bool kVec>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    quantize_t_kernel(const T* __restrict__ x, int rows, int cols, int pitch,
+                      uint8_t* __restrict__ y8, float* __restrict__ scale) {
     extern __shared__ __align__(16) uint8_t q_smem[];
     T* tile = reinterpret_cast<T*>(q_smem);  // [128][128]
     __shared__ float s_col[4][128], s_max[kThreads / 32];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int CB = (cols + 127) / 128;
     const int cb = blockIdx.x % CB, kb = blockIdx.x / CB;  // column and row block of x
-    float all = 0.f;
-    float v[kPerThread][8];
+    if (kVec) {
+        constexpr int PER = 16 / sizeof(T), CHUNKS = 128 / PER;  // 16-byte copies of a row
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-        load_row8(x, rows, cols, vec, kb * 128 + ty + 16 * i, cb * 128 + tx * 8, v[i]);
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        if (!kRowBlocks) all = fmaxf(all, max_abs8(v[i]));
-        store_vec8(tile + (ty + 16 * i) * 128 + tx * 8, v[i]);
-    }
-    if (!kRowBlocks) {
-        all = cta_max(all, s_max);
-        if (threadIdx.x == 0) scale[(size_t)kb * CB + cb] = fp8_scale(all);
+        for (int e = threadIdx.x; e < 128 * CHUNKS; e += kThreads) {
+            const int r = e / CHUNKS, c = e % CHUNKS * PER;
+            T* dst = tile + r * 128 + c;
+            if (kb * 128 + r < rows && cb * 128 + c < cols)
+                sm100::cp_async16(dst, x + (size_t)(kb * 128 + r) * cols + cb * 128 + c);
+            else
+                *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        sm100::cp_async_commit();
+        sm100::cp_async_wait_all();
+    } else {
+#pragma unroll 8
+        for (int e = threadIdx.x; e < 128 * 128; e += kThreads) {
+            const int r = kb * 128 + e / 128, c = cb * 128 + e % 128;
+            tile[e] = r < rows && c < cols ? x[(size_t)r * cols + c] : from_f32<T>(0.f);
+        }
     }
     __syncthreads();
     // two columns of 32 rows
     const int pair = threadIdx.x & 63, rg = threadIdx.x >> 6;
     const int c = cb * 128 + 2 * pair;
-    float f[2];
+    Two<T> v[32];
+    float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+        v[r] = *reinterpret_cast<const Two<T>*>(tile + (rg * 32 + r) * 128 + 2 * pair);
+        max_abs(m, v[r]);
+    }
+    float f0, f1;
     if (kRowBlocks) {
-        float m0 = 0.f, m1 = 0.f;
-#pragma unroll 8
-        for (int r = 0; r < 32; ++r) {
-            const T* p = tile + (rg * 32 + r) * 128 + 2 * pair;
-            m0 = fmaxf(m0, fabsf(to_f32(p[0])));
-            m1 = fmaxf(m1, fabsf(to_f32(p[1])));
-        }
-        s_col[rg][2 * pair] = m0;
-        s_col[rg][2 * pair + 1] = m1;
+        s_col[rg][2 * pair] = m.x;
+        s_col[rg][2 * pair + 1] = m.y;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float m = s_col[0][2 * pair + j];
-#pragma unroll
-            for (int i = 1; i < 4; ++i) m = fmaxf(m, s_col[i][2 * pair + j]);
-            f[j] = fp8_factor(m);
-            if (rg == 0 && c + j < cols) scale[(size_t)kb * cols + c + j] = fp8_scale(m);
+        for (int i = 0; i < 4; ++i) {
+            m.x = fmaxf(m.x, s_col[i][2 * pair]);
+            m.y = fmaxf(m.y, s_col[i][2 * pair + 1]);
+        }
+        f0 = fp8_factor(m.x);
+        f1 = fp8_factor(m.y);
+        if (rg == 0) {
+            if (c < cols) scale[(size_t)kb * cols + c] = fp8_scale(m.x);
+            if (c + 1 < cols) scale[(size_t)kb * cols + c + 1] = fp8_scale(m.y);
         }
     } else {
-        f[0] = f[1] = fp8_factor(all);
-    }
-    uint32_t q0[8], q1[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float a[4], b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const T* p = tile + (rg * 32 + 4 * k + j) * 128 + 2 * pair;
-            a[j] = to_f32(p[0]) * f[0];
-            b[j] = to_f32(p[1]) * f[1];
-        }
-        q0[k] = fp8x4(a[0], a[1], a[2], a[3]);
-        q1[k] = fp8x4(b[0], b[1], b[2], b[3]);
+        const float all = cta_max(fmaxf(m.x, m.y), s_max);
+        if (threadIdx.x == 0) scale[(size_t)kb * CB + cb] = fp8_scale(all);
+        f0 = f1 = fp8_factor(all);
     }
     const int r0 = kb * 128 + rg * 32;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         if (r0 + 16 * half >= pitch) continue;
-        if (c < cols)
-            *reinterpret_cast<uint4*>(y8 + (size_t)c * pitch + r0 + 16 * half) =
-                make_uint4(q0[4 * half], q0[4 * half + 1], q0[4 * half + 2], q0[4 * half + 3]);
+        uint32_t q0[4], q1[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const Two<T>* w = v + 16 * half + 4 * k;
+            q0[k] = fp8x4(w[0].lo() * f0, w[1].lo() * f0, w[2].lo() * f0, w[3].lo() * f0);
+            q1[k] = fp8x4(w[0].hi() * f1, w[1].hi() * f1, w[2].hi() * f1, w[3].hi() * f1);
+        }
+        uint8_t* out = y8 + (size_t)c * pitch + r0 + 16 * half;
+        if (c < cols) *reinterpret_cast<uint4*>(out) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
         if (c + 1 < cols)
-            *reinterpret_cast<uint4*>(y8 + (size_t)(c + 1) * pitch + r0 + 16 * half) =
-                make_uint4(q1[4 * half], q1[4 * half + 1], q1[4 * half + 2], q1[4 * half + 3]);
+            *reinterpret_cast<uint4*>(out + pitch) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
     }
 }
 
-template <typename T, bool kRowBlocks>
+template <typename T, bool kRowBlocks, bool kVec>
 cudaError_t quantize_case(const void* x, int rows, int cols, bool transpose, void* y8,
                           float* scale, cudaStream_t st) {
     const long long tiles = (long long)blocks128(cols) * blocks128(rows);
     if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(tiles);
-    // rows of x start on a 16-byte boundary when cols is a multiple of 8
-    const bool vec = cols % 8 == 0;
     const T* X = static_cast<const T*>(x);
     uint8_t* Y = static_cast<uint8_t*>(y8);
     if (!transpose) {
-        quantize_kernel<T, kRowBlocks>
-            <<<grid, kThreads, 0, st>>>(X, rows, cols, fp8_pitch(cols), vec, Y, scale);
+        quantize_kernel<T, kRowBlocks, kVec>
+            <<<grid, kThreads, 0, st>>>(X, rows, cols, fp8_pitch(cols), Y, scale);
         return cudaGetLastError();
     }
     constexpr int bytes = 128 * 128 * sizeof(T);
-    const cudaError_t e = cudaFuncSetAttribute(quantize_t_kernel<T, kRowBlocks>,
+    const cudaError_t e = cudaFuncSetAttribute(quantize_t_kernel<T, kRowBlocks, kVec>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    quantize_t_kernel<T, kRowBlocks>
-        <<<grid, kThreads, bytes, st>>>(X, rows, cols, fp8_pitch(rows), vec, Y, scale);
+    quantize_t_kernel<T, kRowBlocks, kVec>
+        <<<grid, kThreads, bytes, st>>>(X, rows, cols, fp8_pitch(rows), Y, scale);
     return cudaGetLastError();
+}
+
+// Rows of x start on a 16-byte boundary, and eight columns are all inside or
+// all outside, when cols is a multiple of 8; other sizes load element by element.
+template <typename T>
+cudaError_t quantize_type(const void* x, int rows, int cols, bool row_blocks, bool transpose,
+                          void* y8, float* scale, cudaStream_t st) {
+    if (cols % 8 == 0)
+        return row_blocks ? quantize_case<T, true, true>(x, rows, cols, transpose, y8, scale, st)
+                          : quantize_case<T, false, true>(x, rows, cols, transpose, y8, scale, st);
+    return row_blocks ? quantize_case<T, true, false>(x, rows, cols, transpose, y8, scale, st)
+                      : quantize_case<T, false, false>(x, rows, cols, transpose, y8, scale, st);
 }
 
 }  // namespace
@@ -189,12 +264,9 @@ cudaError_t quantize_case(const void* x, int rows, int cols, bool transpose, voi
 cudaError_t launch_quantize(const void* x, int rows, int cols, kda_dtype_t dt, bool row_blocks,
                             bool transpose, void* y8, float* scale, cudaStream_t st) {
     if (rows == 0) return cudaSuccess;
-    if (dt == KDA_DTYPE_BF16)
-        return row_blocks
-                   ? quantize_case<__nv_bfloat16, true>(x, rows, cols, transpose, y8, scale, st)
-                   : quantize_case<__nv_bfloat16, false>(x, rows, cols, transpose, y8, scale, st);
-    return row_blocks ? quantize_case<float, true>(x, rows, cols, transpose, y8, scale, st)
-                      : quantize_case<float, false>(x, rows, cols, transpose, y8, scale, st);
+    return dt == KDA_DTYPE_BF16
+               ? quantize_type<__nv_bfloat16>(x, rows, cols, row_blocks, transpose, y8, scale, st)
+               : quantize_type<float>(x, rows, cols, row_blocks, transpose, y8, scale, st);
 }
 
 }  // namespace kda
