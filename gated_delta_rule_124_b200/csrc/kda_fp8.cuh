@@ -31,22 +31,37 @@ __device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
     return fp8x2(a, b) | fp8x2(c, d) << 16;
 }
 
-// Eight consecutive elements of a row, from a 16-byte boundary.
-__device__ __forceinline__ void load_vec8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive elements of a row, from a 16-byte boundary, as they lie in
+// memory (a load in flight holds no more registers than its bytes).
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+    uint4 u;
+    __device__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ void get(float (&x)[8]) const {
+        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(v[i] << 16);
-        x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(v[i] << 16);
+            x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        }
     }
-}
-__device__ __forceinline__ void load_vec8(const float* p, float (&x)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+};
+template <>
+struct Vec8<float> {
+    float4 a, b;
+    __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
 __device__ __forceinline__ void store_vec8(__nv_bfloat16* p, const float (&x)[8]) {
     uint32_t v[4];
 #pragma unroll

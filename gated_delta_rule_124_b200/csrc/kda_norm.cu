@@ -10,7 +10,8 @@
 // threads, each with VPT vectors of eight elements (16 bytes of bf16) in
 // registers; vector i of thread t is i TPR + t of the row, so that a block of
 // 128 columns is 16 consecutive lanes and its maximum four shuffles.  CTAs
-// walk over rows and keep w in registers.
+// walk over rows, keep w in registers and request the next row before they
+// reduce the present one.
 //
 // Backward, with r = 1 / sqrt(mean(s^2) + eps):
 //   dx = dsum + r (w dy - s r^2 mean(s w dy))      (also the residual's gradient)
@@ -34,6 +35,9 @@ template <int TPR>
 struct RowGroup {
     static constexpr int kThreads = TPR < 128 ? 128 : TPR;
     static constexpr int kRowsPerCta = kThreads / TPR;
+    // CTAs of an SM (768 threads forward, 512 backward: the registers allow it)
+    static constexpr int kForward = TPR > 512 ? 1 : TPR == 512 ? 1 : 768 / kThreads;
+    static constexpr int kBackward = 512 / kThreads;
 };
 
 // Sum over the TPR threads of a row (every thread gets it).  `buf` holds one
@@ -55,58 +59,88 @@ __device__ __forceinline__ float row_sum(float x, float* buf) {
     return s;
 }
 
+// The same for two sums at once.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float2 x, float2* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+    }
+    if (TPR == 32) return x;
+    constexpr int W = TPR / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) buf[warp] = x;
+    __syncthreads();
+    const float2* mine = buf + warp / W * W;
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        s.x += mine[i].x;
+        s.y += mine[i].y;
+    }
+    return s;
+}
+
 template <typename T>
 __device__ __forceinline__ float stored(float x) { return to_f32(from_f32<T>(x)); }
 
+// A row's vectors of this thread, zeros beyond the row or the last row.
 template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(RowGroup<TPR>::kThreads) add_rms_norm_kernel(
-    const T* x, const T* residual, const float* __restrict__ w, int rows, int D, int pitch,
-    float eps, T* sum, T* y, uint8_t* y8, float* y8_scale) {
-    using G = RowGroup<TPR>;
-    __shared__ float s_part[2][G::kThreads / 32];
-    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float wv[VPT][8];
+__device__ __forceinline__ void load_row(Vec8<T> (&v)[VPT], const T* p, long long row, int rows,
+                                         int D, int t) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * TPR + t) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) wv[i][j] = 0.f;
-        if (c < D) load_vec8(w + c, wv[i]);
+        v[i].zero();
+        if (row < rows && c < D) v[i].load(p + row * D + c);
     }
-    int flip = 0;
-    for (long long base = (long long)blockIdx.x * G::kRowsPerCta; base < rows;
-         base += (long long)gridDim.x * G::kRowsPerCta, flip ^= 1) {
+}
+
+template <typename T, int TPR, int VPT>
+__global__ void __launch_bounds__(RowGroup<TPR>::kThreads, RowGroup<TPR>::kForward)
+    add_rms_norm_kernel(const T* x, const T* residual, const float* __restrict__ w, int rows,
+                        int D, int pitch, float eps, T* sum, T* y, uint8_t* y8, float* y8_scale) {
+    using G = RowGroup<TPR>;
+    __shared__ float s_part[2][G::kThreads / 32];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const long long step = (long long)gridDim.x * G::kRowsPerCta;
+    long long base = (long long)blockIdx.x * G::kRowsPerCta;
+    Vec8<T> xv[VPT], rv[VPT];
+    load_row<T, TPR, VPT>(xv, x, base + sub, rows, D, t);
+    if (residual) load_row<T, TPR, VPT>(rv, residual, base + sub, rows, D, t);
+    float wv[VPT][8];
+    {
+        Vec8<float> q[VPT];
+        load_row<float, TPR, VPT>(q, w, 0, 1, D, t);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) q[i].get(wv[i]);
+    }
+    for (int flip = 0; base < rows; base += step, flip ^= 1) {
         const long long row = base + sub;
         const bool live = row < rows;
         float v[VPT][8];
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * TPR + t) * 8;
+            xv[i].get(v[i]);
+            if (residual) {
+                float r8[8];
+                rv[i].get(r8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-            if (live && c < D) load_vec8(x + row * D + c, v[i]);
+                for (int j = 0; j < 8; ++j) v[i][j] = stored<T>(v[i][j] + r8[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
         }
-        if (residual) {
-            float rv[VPT][8];
+        load_row<T, TPR, VPT>(xv, x, row + step, rows, D, t);
+        if (residual) load_row<T, TPR, VPT>(rv, residual, row + step, rows, D, t);
+        if (sum) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int c = (i * TPR + t) * 8;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) rv[i][j] = 0.f;
-                if (live && c < D) load_vec8(residual + row * D + c, rv[i]);
+                if (live && c < D) store_vec8(sum + row * D + c, v[i]);
             }
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = stored<T>(v[i][j] + rv[i][j]);
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (i * TPR + t) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-            if (sum && live && c < D) store_vec8(sum + row * D + c, v[i]);
         }
         const float r = 1.f / sqrtf(row_sum<TPR>(ss, s_part[flip]) / D + eps);
 #pragma unroll
@@ -128,34 +162,34 @@ __global__ void __launch_bounds__(RowGroup<TPR>::kThreads) add_rms_norm_kernel(
 }
 
 template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(RowGroup<TPR>::kThreads) add_rms_norm_bwd_kernel(
-    const T* __restrict__ s, const float* __restrict__ w, const T* __restrict__ dy,
-    const T* dsum, int rows, int D, float eps, T* dx, float* __restrict__ parts) {
+__global__ void __launch_bounds__(RowGroup<TPR>::kThreads, RowGroup<TPR>::kBackward)
+    add_rms_norm_bwd_kernel(const T* __restrict__ s, const float* __restrict__ w,
+                            const T* __restrict__ dy, const T* dsum, int rows, int D, float eps,
+                            T* dx, float* __restrict__ parts) {
     using G = RowGroup<TPR>;
-    __shared__ float s_part[4][G::kThreads / 32];
+    __shared__ float2 s_part[2][G::kThreads / 32];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const long long step = (long long)gridDim.x * G::kRowsPerCta;
+    long long base = (long long)blockIdx.x * G::kRowsPerCta;
+    // (four vectors a thread leave no registers for the next row's)
+    constexpr bool kAhead = VPT <= 2;
+    Vec8<T> sv[VPT], dv[VPT], av[VPT];
+    auto load_rows = [&](long long row) {
+        load_row<T, TPR, VPT>(sv, s, row, rows, D, t);
+        load_row<T, TPR, VPT>(dv, dy, row, rows, D, t);
+        if (dsum) load_row<T, TPR, VPT>(av, dsum, row, rows, D, t);
+    };
+    if (kAhead) load_rows(base + sub);
     float dw[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-    int flip = 0;
-    for (long long base = (long long)blockIdx.x * G::kRowsPerCta; base < rows;
-         base += (long long)gridDim.x * G::kRowsPerCta, flip ^= 2) {
+    for (int flip = 0; base < rows; base += step, flip ^= 1) {
         const long long row = base + sub;
         const bool live = row < rows;
+        if (!kAhead) load_rows(row);
         float v[VPT][8], d[VPT][8], add[VPT][8];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = (i * TPR + t) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = d[i][j] = add[i][j] = 0.f;
-            if (live && c < D) {
-                load_vec8(s + row * D + c, v[i]);
-                load_vec8(dy + row * D + c, d[i]);
-                if (dsum) load_vec8(dsum + row * D + c, add[i]);
-            }
-        }
         float ss = 0.f, sd = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -165,14 +199,21 @@ __global__ void __launch_bounds__(RowGroup<TPR>::kThreads) add_rms_norm_bwd_kern
                 *reinterpret_cast<float4*>(wv) = *reinterpret_cast<const float4*>(w + c);
                 *reinterpret_cast<float4*>(wv + 4) = *reinterpret_cast<const float4*>(w + c + 4);
             }
+            sv[i].get(v[i]);
+            dv[i].get(d[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) add[i][j] = 0.f;
+            if (dsum) av[i].get(add[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 ss = fmaf(v[i][j], v[i][j], ss);
                 sd = fmaf(v[i][j], wv[j] * d[i][j], sd);
             }
         }
-        const float r = 1.f / sqrtf(row_sum<TPR>(ss, s_part[flip]) / D + eps);
-        const float m = r * r * (row_sum<TPR>(sd, s_part[flip + 1]) / D);
+        // (dsum may be dx: a row is written by the threads that read it)
+        if (kAhead) load_rows(row + step);
+        const float2 sums = row_sum<TPR>(make_float2(ss, sd), s_part[flip]);
+        const float r = 1.f / sqrtf(sums.x / D + eps), m = r * r * (sums.y / D);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * TPR + t) * 8;
@@ -221,21 +262,15 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
     }
 }
 
-// CTAs that walk over `rows` rows, `most` at most (0: as many as fit on the device).
-template <typename K>
-cudaError_t walkers(K kernel, int threads, int rows, int rows_per_cta, int most, unsigned* grid) {
-    long long ctas = ((long long)rows + rows_per_cta - 1) / rows_per_cta;
-    if (most == 0) {
-        int dev = 0, sms = 0, per_sm = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
-        if (e != cudaSuccess) return e;
-        most = sms * (per_sm > 0 ? per_sm : 1);
-    }
+// CTAs that walk over `rows` rows: as many as fit on the device, `per_sm` each.
+cudaError_t walkers(int rows, int rows_per_cta, int per_sm, unsigned* grid) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long long ctas = ((long long)rows + rows_per_cta - 1) / rows_per_cta;
+    const long long most = (long long)sms * per_sm;
     *grid = static_cast<unsigned>(ctas < most ? ctas : most);
-    return cudaSuccess;
+    return e;
 }
 
 template <typename T, int TPR, int VPT>
@@ -243,8 +278,7 @@ cudaError_t norm_case(const void* x, const void* residual, const float* w, int r
                       float eps, void* sum, void* y, void* y8, float* y8_scale, cudaStream_t st) {
     using G = RowGroup<TPR>;
     unsigned grid = 0;
-    const cudaError_t e = walkers(add_rms_norm_kernel<T, TPR, VPT>, G::kThreads, rows,
-                                  G::kRowsPerCta, 0, &grid);
+    const cudaError_t e = walkers(rows, G::kRowsPerCta, G::kForward, &grid);
     if (e != cudaSuccess) return e;
     add_rms_norm_kernel<T, TPR, VPT><<<grid, G::kThreads, 0, st>>>(
         static_cast<const T*>(x), static_cast<const T*>(residual), w, rows, D, fp8_pitch(D), eps,
@@ -257,10 +291,9 @@ cudaError_t norm_bwd_case(const void* s, const float* w, const void* dy, const v
                           int rows, int D, float eps, void* dx, float* dw, void* ws,
                           cudaStream_t st) {
     using G = RowGroup<TPR>;
-    unsigned grid = 0;
-    const cudaError_t e = walkers(add_rms_norm_bwd_kernel<T, TPR, VPT>, G::kThreads, rows,
-                                  G::kRowsPerCta, kMaxParts / G::kRowsPerCta, &grid);
-    if (e != cudaSuccess) return e;
+    constexpr int most = kMaxParts / G::kRowsPerCta;
+    const int ctas = (rows + G::kRowsPerCta - 1) / G::kRowsPerCta;
+    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
     float* parts = static_cast<float*>(ws);
     if (grid > 0)
         add_rms_norm_bwd_kernel<T, TPR, VPT><<<grid, G::kThreads, 0, st>>>(
