@@ -121,16 +121,35 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&o)[4]) {
 template <typename T>
 __device__ __forceinline__ void put(T* p, const float (&o)[1]) { *p = from_f32<T>(o[0]); }
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// h times 2^G, also where 2^G alone leaves the fp32 range.
-__device__ __forceinline__ float scaled(float h, float G) {
-    const float e = exp2f(0.5f * G);
-    return h == 0.f ? 0.f : (h * e) * e;  // (0 times a product that overflows is 0)
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-// The state after a map (G, b) applied to h; G = -inf: the map forgets h.
-__device__ __forceinline__ float applied(float G, float b, float h) {
-    return G == -INFINITY ? b : b + scaled(h, G);
+// exp(g), and its logarithm to base 2 added to G: 2^y (1 + r ln 2) with y + r =
+// g log2(e) in two floats, so that the error stays that of ex2 (2 units in the
+// last place) for every g.
+__device__ __forceinline__ float gate(float g, float& G) {
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299e-8f;  // log2(e)
+    constexpr float kLn2 = 0.693147182464599609375f;
+    const float y = g * kHi;
+    const float r = fmaf(g, kHi, -y) + g * kLo;
+    G += y;
+    const float e = ex2(y);
+    return fmaf(e, r * kLn2, e);
+}
+
+// A state times 2^G is (h e) e with e = 2^(G / 2), so that a product of gates
+// beyond the fp32 range times a small state is still right (and 0 times a
+// product that overflows is 0).
+__device__ __forceinline__ float scaled(float h, float e) { return h == 0.f ? 0.f : (h * e) * e; }
+// e of a map; negative for one that forgets the state before it (G = -inf).
+__device__ __forceinline__ float half_gate(float G) {
+    return G == -INFINITY ? -1.f : ex2(0.5f * G);
+}
+// The state after a map (e, b) applied to h.
+__device__ __forceinline__ float applied(float e, float b, float h) {
+    return e < 0.f ? b : b + scaled(h, e);
 }
 
 __device__ __forceinline__ void publish(uint64_t* w, float G, float b, bool exit_state) {
@@ -170,7 +189,7 @@ __device__ float look_back(const uint64_t* words, size_t C, int first, int step,
             }
             const uint32_t lo = static_cast<uint32_t>(v[j]);
             const float b = __uint_as_float(static_cast<uint32_t>(v[j] >> 32));
-            h += scaled(b, G);
+            h += scaled(b, ex2(0.5f * G));
             if (lo == kExit) return h;
             G += __uint_as_float(lo);
         }
@@ -178,37 +197,51 @@ __device__ float look_back(const uint64_t* words, size_t C, int first, int step,
     return h;
 }
 
-// Sequence bounds inside the tile's rows: first_of[r] = the sequence whose first
+// Where the tile's sequences begin and end: first_of[r] = the sequence whose first
 // token is row r, last_of[r] = the one whose last token it is, -1 elsewhere.
 // Reads of cu stay inside [0, N] and writes inside the tile whatever cu holds.
-__device__ __forceinline__ void mark_bounds(const ScanArgs& a, int t0, int* first_of,
-                                            int* last_of) {
-    for (int r = threadIdx.x; r < kRows; r += kThreads) first_of[r] = last_of[r] = -1;
-    int lo;  // the last sequence whose first token is at or before t0
-    if (!a.cu) {
-        lo = a.T > 0 ? t0 / a.T : 0;
-    } else {  // every warp searches for itself, 32 offsets at a time
-        const int lane = threadIdx.x & 31;
-        lo = 0;
-        int span = a.N;
-        while (true) {
-            const int step = span <= 32 ? 1 : (span + 31) / 32;
-            const int idx = lo + lane * step;
-            const bool le = idx < lo + span && idx < a.N && a.cu[idx] <= t0;
-            const unsigned m = __ballot_sync(0xffffffffu, le);
-            lo += (m ? 31 - __clz(static_cast<int>(m)) : 0) * step;
-            if (step == 1) break;
-            span = min(step, a.N - lo);
+struct Bounds {
+    int first_of[kRows], last_of[kRows];
+    int lo;      // the last sequence whose first token is at or before the tile
+    int plain;   // the tile lies inside one sequence, which goes on beyond both ends
+};
+// By every thread of the CTA; ends with a barrier.
+__device__ __forceinline__ void find_bounds(const ScanArgs& a, int t0, Bounds& s) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int lo = 0;
+        if (!a.cu) {
+            lo = a.T > 0 ? t0 / a.T : 0;
+        } else {  // 32 offsets at a time
+            int span = a.N;
+            while (true) {
+                const int step = span <= 32 ? 1 : (span + 31) / 32;
+                const int idx = lo + lane * step;
+                const bool le = idx < lo + span && idx < a.N && a.cu[idx] <= t0;
+                const unsigned m = __ballot_sync(0xffffffffu, le);
+                lo += (m ? 31 - __clz(static_cast<int>(m)) : 0) * step;
+                if (step == 1) break;
+                span = min(step, a.N - lo);
+            }
+        }
+        if (lane == 0) {
+            const int b = a.cu ? a.cu[lo] : lo * a.T;
+            const int e = a.cu ? a.cu[lo + 1] : (lo + 1) * a.T;
+            s.lo = lo;
+            s.plain = b < t0 && e > t0 + kRows && t0 + kRows <= a.total;
         }
     }
     __syncthreads();
-    for (int i = lo + threadIdx.x; i < a.N; i += kThreads) {
+    if (s.plain) return;
+    for (int r = threadIdx.x; r < kRows; r += kThreads) s.first_of[r] = s.last_of[r] = -1;
+    __syncthreads();
+    for (int i = s.lo + threadIdx.x; i < a.N; i += kThreads) {
         const int b = (a.cu ? a.cu[i] : i * a.T) - t0;
         if (b >= kRows) break;
         const int e = (a.cu ? a.cu[i + 1] : (i + 1) * a.T) - t0;
         if (e <= b) continue;  // an empty sequence has no token
-        if (b >= 0) first_of[b] = i;
-        if (e >= 1 && e <= kRows) last_of[e - 1] = i;
+        if (b >= 0) s.first_of[b] = i;
+        if (e >= 1 && e <= kRows) s.last_of[e - 1] = i;
     }
     __syncthreads();
 }
@@ -248,166 +281,71 @@ __device__ __forceinline__ int next_tile(const ScanArgs& a) {
     return static_cast<int>(s_ticket);
 }
 
-template <int VEC, typename T>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanArgs a) {
-    constexpr int CT = 32 * VEC;  // channels of a tile
-    __shared__ __align__(16) float s_G[kWarps][CT], s_b[kWarps][CT];
-    __shared__ int s_first[kRows], s_last[kRows];
-
-    const int task = next_tile(a), tile = task / a.ctiles, c0 = (task % a.ctiles) * CT;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = c0 + lane * VEC, t0 = tile * kRows;
-    const bool mine = c < a.C;
-    const size_t C = a.C;
-
-    // 1. the whole tile into registers
-    Raw<VEC, T> xr[kR];
-    Raw<VEC, float> gr[kR];
+// A warp's rows of a tile in registers.  Lanes beyond the last channel load the
+// last ones again (they store nothing); rows beyond the last token hold zeros,
+// which change no state.
+template <int VEC, typename U>
+__device__ __forceinline__ void load_rows(Raw<VEC, U> (&v)[kR], const U* p, size_t C, int rows) {
+    if (rows >= kR) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const int t = t0 + w * kR + r;
-        xr[r].zero();
-        gr[r].zero();
-        if (mine && t < a.total) {
-            xr[r].load(static_cast<const T*>(a.x) + (size_t)t * C + c);
-            gr[r].load(a.g + (size_t)t * C + c);
-        }
-    }
-    mark_bounds(a, t0, s_first, s_last);
-    if (tile == 0) {
-        if (c0 == 0) report_status(a);
-        pass_empty(a, a.h0, a.final_state, c0, min(CT, a.C - c0));
-    }
-
-    // 2. the map of this warp's rows
-    float al[kR][VEC], G[VEC], b[VEC];
+        for (int r = 0; r < kR; ++r) v[r].load(p + r * C);
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const int first = s_first[w * kR + r];
-        float gv[VEC], xv[VEC];
-        gr[r].get(gv);
-        xr[r].get(xv);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            al[r][j] = expf(gv[j]);
-            G[j] = fmaf(gv[j], kLog2e, G[j]);
-        }
-        if (first >= 0) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                G[j] = -INFINITY;
-                b[j] = a.h0 && mine ? a.h0[(size_t)first * C + c + j] : 0.f;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[r][j], b[j], xv[j]);
-        // from here on a first row's al is its state: initial_state is read
-        // before this tile publishes anything, so that final_state may be the
-        // same buffer
-        if (first >= 0) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) al[r][j] = b[j];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        s_G[w][lane * VEC + j] = G[j];
-        s_b[w][lane * VEC + j] = b[j];
-    }
-    __syncthreads();
-
-    // 3. one thread per channel: the tile's map out, its entry state in, every
-    // warp's entry state
-    if (threadIdx.x < CT && c0 + threadIdx.x < a.C) {
-        const int ch = threadIdx.x;
-        const bool last_tile = tile == a.tiles - 1;
-        float Gt = 0.f, bt = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            bt = applied(s_G[i][ch], s_b[i][ch], bt);
-            Gt += s_G[i][ch];
-        }
-        float h = 0.f;
-        if (a.ticket) {
-            uint64_t* out = a.words + (size_t)tile * C + c0 + ch;
-            const bool known = tile == 0 || Gt == -INFINITY;
-            if (!last_tile) publish(out, Gt, bt, known);
-            // the entry state is used unless a sequence starts with the tile
-            if (tile > 0 && s_first[0] < 0) {
-                h = look_back(a.words + c0 + ch, C, tile - 1, -1, tile, a.status);
-                if (!known && !last_tile) publish(out, 0.f, applied(Gt, bt, h), true);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const float Gi = s_G[i][ch], bi = s_b[i][ch];
-            s_b[i][ch] = h;
-            h = applied(Gi, bi, h);
-        }
-        if (a.entry) a.entry[(size_t)tile * C + c0 + ch] = s_b[0][ch];
-    }
-    if (!a.h && !a.final_state) return;
-    __syncthreads();
-
-    // 4. the recurrence from this warp's entry state
-    if (!mine) return;
-    float h[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = s_b[w][lane * VEC + j];
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const int t = t0 + w * kR + r;
-        if (t >= a.total) return;
-        const int first = s_first[w * kR + r], last = s_last[w * kR + r];
-        float xv[VEC];
-        xr[r].get(xv);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] = first >= 0 ? al[r][j] : fmaf(al[r][j], h[j], xv[j]);
-        if (a.h) put(static_cast<T*>(a.h) + (size_t)t * C + c, h);
-        if (last >= 0 && a.final_state) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) a.final_state[(size_t)last * C + c + j] = h[j];
+        for (int r = 0; r < kR; ++r) {
+            v[r].zero();
+            if (r < rows) v[r].load(p + r * C);
         }
     }
 }
-
-template <int VEC, typename T>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanArgs a) {
-    constexpr int CT = 32 * VEC;
-    __shared__ __align__(16) float s_G[kWarps][CT], s_b[kWarps][CT];    // forward maps
-    __shared__ __align__(16) float s_Ge[kWarps][CT], s_e[kWarps][CT];   // maps of e, from the right
-    __shared__ int s_first[kRows], s_last[kRows];
-
-    const int task = next_tile(a), tile = a.tiles - 1 - task / a.ctiles;
-    const int c0 = (task % a.ctiles) * CT;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = c0 + lane * VEC, t0 = tile * kRows;
-    const bool mine = c < a.C;
-    const size_t C = a.C;
-
-    Raw<VEC, T> xr[kR], dr[kR];
-    Raw<VEC, float> gr[kR];
+template <int VEC>
+__device__ __forceinline__ void state_of(const float* states, int seq, size_t C, int c,
+                                         float (&v)[VEC]) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const int t = t0 + w * kR + r;
-        xr[r].zero();
-        dr[r].zero();
-        gr[r].zero();
-        if (mine && t < a.total) {
-            xr[r].load(static_cast<const T*>(a.x) + (size_t)t * C + c);
-            gr[r].load(a.g + (size_t)t * C + c);
-            dr[r].load(static_cast<const T*>(a.dout) + (size_t)t * C + c);
+    for (int j = 0; j < VEC; ++j) v[j] = states ? states[(size_t)seq * C + c + j] : 0.f;
+}
+
+// Shared memory of a tile: the warps' maps and, in the end, the states that
+// enter the warps.
+template <int VEC>
+struct Maps {
+    float G[kWarps][32 * VEC], e[kWarps][32 * VEC], b[kWarps][32 * VEC];
+    __device__ void set(int w, int lane, const float (&g)[VEC], const float (&v)[VEC]) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            G[w][lane * VEC + j] = g[j];
+            e[w][lane * VEC + j] = half_gate(g[j]);
+            b[w][lane * VEC + j] = v[j];
         }
     }
-    mark_bounds(a, t0, s_first, s_last);
-    if (tile == a.tiles - 1) {
-        if (c0 == 0) report_status(a);
-        pass_empty(a, a.dfinal, a.dh0, c0, min(CT, a.C - c0));
+    __device__ float sum(int ch) const {
+        float g = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) g += G[i][ch];
+        return g;
     }
+    // Walks a channel's state through the warps (from the last one if
+    // kReverse); kKeep: leaves in b what enters each.  Returns what leaves.
+    template <bool kReverse, bool kKeep>
+    __device__ float walk(int ch, float h) {
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const int i = kReverse ? kWarps - 1 - k : k;
+            const float bi = b[i][ch];
+            if (kKeep) b[i][ch] = h;
+            h = applied(e[i][ch], bi, h);
+        }
+        return h;
+    }
+};
 
-    // the two maps of this warp's rows
+// kBounds: sequences begin or end in the tile, or the tokens do.
+template <int VEC, typename T, bool kBounds>
+__device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Maps<VEC>& s_maps,
+                                         const Bounds& s_bounds, const Raw<VEC, T> (&xr)[kR],
+                                         const Raw<VEC, float> (&gr)[kR], int c, bool mine) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = tile * kRows;
+    const size_t C = a.C;
+    // the map of this warp's rows
     float al[kR][VEC];
     {
         float G[VEC], b[VEC];
@@ -415,90 +353,176 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanArgs a) {
         for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            const int first = s_first[w * kR + r];
             float gv[VEC], xv[VEC];
             gr[r].get(gv);
             xr[r].get(xv);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                al[r][j] = expf(gv[j]);
-                G[j] = fmaf(gv[j], kLog2e, G[j]);
-            }
-            if (first >= 0) {
+            for (int j = 0; j < VEC; ++j) al[r][j] = gate(gv[j], G[j]);
+            const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+            if (kBounds && first >= 0) {
+                state_of<VEC>(a.h0, first, C, c, b);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    G[j] = -INFINITY;
-                    b[j] = a.h0 && mine ? a.h0[(size_t)first * C + c + j] : 0.f;
-                }
+                for (int j = 0; j < VEC; ++j) G[j] = -INFINITY;
             }
 #pragma unroll
             for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[r][j], b[j], xv[j]);
-        }
+            // from here on a first row's al is its state: initial_state is read
+            // before this tile publishes anything, so that final_state may be
+            // the same buffer
+            if (kBounds && first >= 0) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            s_G[w][lane * VEC + j] = G[j];
-            s_b[w][lane * VEC + j] = b[j];
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
-#pragma unroll
-        for (int r = kR - 1; r >= 0; --r) {
-            const int last = s_last[w * kR + r];
-            float gv[VEC], dv[VEC];
-            gr[r].get(gv);
-            dr[r].get(dv);
-            if (last >= 0) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    G[j] = -INFINITY;
-                    b[j] = a.dfinal && mine ? a.dfinal[(size_t)last * C + c + j] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                b[j] = al[r][j] * (dv[j] + b[j]);
-                G[j] = fmaf(gv[j], kLog2e, G[j]);
+                for (int j = 0; j < VEC; ++j) al[r][j] = b[j];
             }
         }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            s_Ge[w][lane * VEC + j] = G[j];
-            s_e[w][lane * VEC + j] = b[j];
-        }
+        s_maps.set(w, lane, G, b);
     }
     __syncthreads();
 
-    if (threadIdx.x < CT && c0 + threadIdx.x < a.C) {
+    // one thread per channel: the tile's map out, its entry state in, every
+    // warp's entry state
+    if (threadIdx.x < 32 * VEC && c0 + threadIdx.x < a.C) {
         const int ch = threadIdx.x;
-        float Gt = 0.f, bt = 0.f;
-#pragma unroll
-        for (int i = kWarps - 1; i >= 0; --i) {
-            bt = applied(s_Ge[i][ch], s_e[i][ch], bt);
-            Gt += s_Ge[i][ch];
-        }
-        float e = 0.f;
+        const bool last_tile = tile == a.tiles - 1;
+        float h = 0.f;
         if (a.ticket) {
             uint64_t* out = a.words + (size_t)tile * C + c0 + ch;
-            const bool known = tile == a.tiles - 1 || Gt == -INFINITY;
-            if (tile > 0) publish(out, Gt, bt, known);
-            if (tile < a.tiles - 1 && s_last[kRows - 1] < 0) {
-                e = look_back(a.words + c0 + ch, C, tile + 1, 1, a.tiles - 1 - tile, a.status);
-                if (!known && tile > 0) publish(out, 0.f, applied(Gt, bt, e), true);
+            const float Gt = s_maps.sum(ch), bt = s_maps.template walk<false, false>(ch, 0.f);
+            const bool known = tile == 0 || Gt == -INFINITY;
+            if (!last_tile) publish(out, Gt, bt, known);
+            // the entry state is used unless a sequence starts with the tile
+            if (tile > 0 && !(kBounds && s_bounds.first_of[0] >= 0)) {
+                h = look_back(a.words + c0 + ch, C, tile - 1, -1, tile, a.status);
+                if (!known && !last_tile)
+                    publish(out, 0.f, applied(half_gate(Gt), bt, h), true);
+            }
+        }
+        s_maps.template walk<false, true>(ch, h);
+        if (a.entry) a.entry[(size_t)tile * C + c0 + ch] = h;
+    }
+    if (!a.h && !a.final_state) return;
+    __syncthreads();
+
+    // the recurrence from this warp's entry state
+    if (!mine) return;
+    float h[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) h[j] = s_maps.b[w][lane * VEC + j];
+    T* out = static_cast<T*>(a.h) + (size_t)(t0 + w * kR) * C + c;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        if (kBounds && t0 + w * kR + r >= a.total) return;
+        const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+        float xv[VEC];
+        xr[r].get(xv);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            h[j] = kBounds && first >= 0 ? al[r][j] : fmaf(al[r][j], h[j], xv[j]);
+        if (a.h) put(out + r * C, h);
+        const int last = kBounds ? s_bounds.last_of[w * kR + r] : -1;
+        if (kBounds && last >= 0 && a.final_state) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) a.final_state[(size_t)last * C + c + j] = h[j];
+        }
+    }
+}
+
+template <int VEC, typename T>
+__global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs a) {
+    constexpr int CT = 32 * VEC;  // channels of a tile
+    __shared__ __align__(16) Maps<VEC> s_maps;
+    __shared__ Bounds s_bounds;
+    const int task = next_tile(a), tile = task / a.ctiles, c0 = (task % a.ctiles) * CT;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = tile * kRows + w * kR, mine = c0 + lane * VEC < a.C;
+    const int c = mine ? c0 + lane * VEC : a.C - VEC;
+    Raw<VEC, T> xr[kR];
+    Raw<VEC, float> gr[kR];
+    load_rows(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C, a.total - t);
+    load_rows(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
+    find_bounds(a, tile * kRows, s_bounds);
+    if (tile == 0) {
+        if (c0 == 0) report_status(a);
+        pass_empty(a, a.h0, a.final_state, c0, min(CT, a.C - c0));
+    }
+    if (s_bounds.plain)
+        fwd_tile<VEC, T, false>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+    else
+        fwd_tile<VEC, T, true>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+}
+
+template <int VEC, typename T, bool kBounds>
+__device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Maps<VEC>& s_maps,
+                                         Maps<VEC>& s_back, const Bounds& s_bounds,
+                                         const Raw<VEC, T> (&xr)[kR], const Raw<VEC, T> (&dr)[kR],
+                                         const Raw<VEC, float> (&gr)[kR], int c, bool mine) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = tile * kRows;
+    const size_t C = a.C;
+    // the two maps of this warp's rows: of h, and of e from the right
+    float al[kR][VEC];
+    {
+        float G[VEC], Ge[VEC], b[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            float gv[VEC], xv[VEC];
+            gr[r].get(gv);
+            xr[r].get(xv);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) al[r][j] = gate(gv[j], G[j]);
+            const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+            if (kBounds && first >= 0) state_of<VEC>(a.h0, first, C, c, b);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[r][j], b[j], xv[j]);
+        }
+        bool starts = false, ends = false;
+        if (kBounds) {
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                starts |= s_bounds.first_of[w * kR + r] >= 0;
+                ends |= s_bounds.last_of[w * kR + r] >= 0;
             }
         }
 #pragma unroll
-        for (int i = kWarps - 1; i >= 0; --i) {
-            const float Gi = s_Ge[i][ch], bi = s_e[i][ch];
-            s_e[i][ch] = e;
-            e = applied(Gi, bi, e);
+        for (int j = 0; j < VEC; ++j) {
+            Ge[j] = kBounds && ends ? -INFINITY : G[j];
+            if (kBounds && starts) G[j] = -INFINITY;
         }
-        float h = a.entry[(size_t)tile * C + c0 + ch];
+        s_maps.set(w, lane, G, b);
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const float Gi = s_G[i][ch], bi = s_b[i][ch];
-            s_b[i][ch] = h;
-            h = applied(Gi, bi, h);
+        for (int j = 0; j < VEC; ++j) b[j] = 0.f;
+#pragma unroll
+        for (int r = kR - 1; r >= 0; --r) {
+            const int last = kBounds ? s_bounds.last_of[w * kR + r] : -1;
+            if (kBounds && last >= 0) state_of<VEC>(a.dfinal, last, C, c, b);
+            float dv[VEC];
+            dr[r].get(dv);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) b[j] = al[r][j] * (dv[j] + b[j]);
         }
+        s_back.set(w, lane, Ge, b);
+    }
+    __syncthreads();
+
+    if (threadIdx.x < 32 * VEC && c0 + threadIdx.x < a.C) {
+        const int ch = threadIdx.x;
+        float e = 0.f;
+        if (a.ticket) {
+            uint64_t* out = a.words + (size_t)tile * C + c0 + ch;
+            const float Gt = s_back.sum(ch), bt = s_back.template walk<true, false>(ch, 0.f);
+            const bool known = tile == a.tiles - 1 || Gt == -INFINITY;
+            if (tile > 0) publish(out, Gt, bt, known);
+            if (tile < a.tiles - 1 && !(kBounds && s_bounds.last_of[kRows - 1] >= 0)) {
+                e = look_back(a.words + c0 + ch, C, tile + 1, 1, a.tiles - 1 - tile, a.status);
+                if (!known && tile > 0)
+                    publish(out, 0.f, applied(half_gate(Gt), bt, e), true);
+            }
+        }
+        s_back.template walk<true, true>(ch, e);
+    } else if (threadIdx.x >= kThreads - 32 * VEC && c0 + threadIdx.x - (kThreads - 32 * VEC) < a.C) {
+        // meanwhile (other warps): the states that enter the warps
+        const int ch = threadIdx.x - (kThreads - 32 * VEC);
+        s_maps.template walk<false, true>(ch, a.entry[(size_t)tile * C + c0 + ch]);
     }
     __syncthreads();
 
@@ -506,16 +530,13 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanArgs a) {
     float hb[kR][VEC], h[VEC], e[VEC];  // hb: the state before each row
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        h[j] = s_b[w][lane * VEC + j];
-        e[j] = s_e[w][lane * VEC + j];
+        h[j] = s_maps.b[w][lane * VEC + j];
+        e[j] = s_back.b[w][lane * VEC + j];
     }
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-        const int first = s_first[w * kR + r];
-        if (first >= 0) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) h[j] = a.h0 ? a.h0[(size_t)first * C + c + j] : 0.f;
-        }
+        const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+        if (kBounds && first >= 0) state_of<VEC>(a.h0, first, C, c, h);
         float xv[VEC];
         xr[r].get(xv);
 #pragma unroll
@@ -524,16 +545,13 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanArgs a) {
             h[j] = fmaf(al[r][j], h[j], xv[j]);
         }
     }
+    T* dx = static_cast<T*>(a.dx) + (size_t)(t0 + w * kR) * C + c;
+    float* dg = a.dg + (size_t)(t0 + w * kR) * C + c;
 #pragma unroll
     for (int r = kR - 1; r >= 0; --r) {
-        const int t = t0 + w * kR + r;
-        if (t >= a.total) continue;
-        const int first = s_first[w * kR + r], last = s_last[w * kR + r];
-        if (last >= 0) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                e[j] = a.dfinal ? a.dfinal[(size_t)last * C + c + j] : 0.f;
-        }
+        if (kBounds && t0 + w * kR + r >= a.total) continue;
+        const int last = kBounds ? s_bounds.last_of[w * kR + r] : -1;
+        if (kBounds && last >= 0) state_of<VEC>(a.dfinal, last, C, c, e);
         float dv[VEC], dgv[VEC];
         dr[r].get(dv);
 #pragma unroll
@@ -542,13 +560,40 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanArgs a) {
             e[j] = al[r][j] * dv[j];
             dgv[j] = e[j] * hb[r][j];
         }
-        put(static_cast<T*>(a.dx) + (size_t)t * C + c, dv);
-        put(a.dg + (size_t)t * C + c, dgv);
-        if (first >= 0 && a.dh0) {
+        put(dx + r * C, dv);
+        put(dg + r * C, dgv);
+        const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+        if (kBounds && first >= 0 && a.dh0) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) a.dh0[(size_t)first * C + c + j] = e[j];
         }
     }
+}
+
+template <int VEC, typename T>
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a) {
+    constexpr int CT = 32 * VEC;
+    __shared__ __align__(16) Maps<VEC> s_maps, s_back;
+    __shared__ Bounds s_bounds;
+    const int task = next_tile(a), tile = a.tiles - 1 - task / a.ctiles;
+    const int c0 = (task % a.ctiles) * CT;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = tile * kRows + w * kR, mine = c0 + lane * VEC < a.C;
+    const int c = mine ? c0 + lane * VEC : a.C - VEC;
+    Raw<VEC, T> xr[kR], dr[kR];
+    Raw<VEC, float> gr[kR];
+    load_rows(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
+    load_rows(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C, a.total - t);
+    load_rows(dr, static_cast<const T*>(a.dout) + (size_t)t * a.C + c, a.C, a.total - t);
+    find_bounds(a, tile * kRows, s_bounds);
+    if (tile == a.tiles - 1) {
+        if (c0 == 0) report_status(a);
+        pass_empty(a, a.dfinal, a.dh0, c0, min(CT, a.C - c0));
+    }
+    if (s_bounds.plain)
+        bwd_tile<VEC, T, false>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
+    else
+        bwd_tile<VEC, T, true>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
 }
 
 // One token per sequence: state = exp(g) state + x, h = the state in T.

@@ -11,11 +11,9 @@ with the tile's part by 2 u: 64 u M more at each tile.  bf16 outputs are one
 rounding further, 2^-8 of the value.  Gradients obey the same recurrence from the
 other side; dg is e_t h_{t-1}, a product of two such values.
 
-Below 2^-126 roundings are absolute: half a step of fp32's subnormal numbers,
-2^-150.  A step rounds its product (2^-150) and its gate (2 steps of 2^-149, times
-a state of at most 16 here): 65 x 2^-150, which the next steps do not increase
-where gates are that small; two such values meet in dg, each with a factor of at
-most 16.  Together below 2 x 16 x 65 x 2^-150 < 2^-138."""
+Below 2^-126 errors are absolute: a gate that small may be taken as zero, 2^-126
+times a state (at most 16 here), and in dg once more times a state: 2^-118; fp32's
+subnormal roundings (2^-150 each) are far below that."""
 import numpy as np
 import pytest
 import torch
@@ -26,7 +24,7 @@ from oracle import scan as oscan
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
-TINY = 2.0 ** -138
+TINY = 2.0 ** -117
 BF16 = 2.0 ** -8
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 TILE = 64
