@@ -14,6 +14,7 @@ workspace with PyTorch and then make the same calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -155,22 +156,15 @@ def _p(t) -> int | None:
 _TORCH_OF = {KDA_DTYPE_F32: torch.float32, KDA_DTYPE_BF16: torch.bfloat16}
 
 
-_FP8_BYTES = (torch.float8_e4m3fn, torch.uint8)
-
-
-def _check(what, dtype=None, typed=(), f32=(), i32=(), raw=(), f8=()):
+def _check(what, dtype=None, typed=(), f32=(), i32=(), raw=()):
     """Reject tensors the C ABI would misread, before any pointer is passed:
     every tensor must be contiguous and on one device; `typed` tensors (q, k,
     v, o, dout ...) must have the call's dtype, `f32` ones (g, beta, states,
-    gradients) float32, `i32` ones (cu_seqlens) int32, `f8` ones (e4m3 codes)
-    float8_e4m3fn or uint8; `raw` ones (workspaces) only contiguous.  Plain ints (raw addresses) and None are not checked."""
+    gradients) float32, `i32` ones (cu_seqlens) int32; `raw` ones (workspaces)
+    only contiguous.  Plain ints (raw addresses) and None are not checked."""
     want = None if dtype is None else _TORCH_OF[dtype_code(dtype)]
     dev = None
-    for t in f8:
-        if isinstance(t, torch.Tensor) and t.dtype not in _FP8_BYTES:
-            raise ValueError(f"{what}: expected float8_e4m3fn or uint8, got {t.dtype}")
-    for group, need in ((typed, want), (f32, torch.float32), (i32, torch.int32), (raw, None),
-                        (f8, None)):
+    for group, need in ((typed, want), (f32, torch.float32), (i32, torch.int32), (raw, None)):
         for t in group:
             if t is None or isinstance(t, int):
                 continue
@@ -197,16 +191,56 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
-def _enqueue(name, tensor, stream, check, *args) -> int:
-    """The library's call `name` with `args` and the stream: the given one, or
-    the current stream of `tensor`'s device, which is the current device during
-    the call."""
-    fn = getattr(load(), name)
-    dev = tensor.device if isinstance(tensor, torch.Tensor) else None
-    if dev is None or dev.type != "cuda" or dev.index == torch.cuda.current_device():
+_F32, _I32, _ANY = (torch.float32,), (torch.int32,), None
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _args(what, *pairs):
+    """The device pointers of (tensor, the dtypes it may have) pairs, and the index
+    of the tensors' device: _check's rules in one pass, for calls short enough
+    that a decode step waits for the host.  None and raw addresses pass through."""
+    device, out = None, []
+    for t, need in pairs:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{what}: expected a tensor, got {type(t).__name__}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: every tensor must be contiguous (got strides "
+                             f"{tuple(t.stride())} for shape {tuple(t.shape)})")
+        if need is not None and t.dtype not in need:
+            raise ValueError(f"{what}: expected {' or '.join(map(str, need))}, got {t.dtype}")
+        d = t.get_device()
+        if device is None:
+            device = d
+        elif d != device:
+            raise ValueError(f"{what}: tensors on different devices ({device} and {d})")
+        out.append(t.data_ptr())
+    return out, device
+
+
+# The handle of a device's current stream (without the object around it, where
+# this torch offers that).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _enqueue(name, device, stream, check, *args) -> int:
+    """The library's call `name` with `args` and a stream: the given one, or the
+    current stream of the tensors' device, which is the current device during the
+    call."""
+    fn = getattr(_lib or load(), name)
+    if device is None or device < 0:   # raw addresses, or nothing on a GPU
         return _ret(fn(*args, _stream(stream)), name, check)
-    with torch.cuda.device(dev):
-        return _ret(fn(*args, _stream(stream)), name, check)
+    if stream is None:
+        stream = _current_stream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        return _ret(fn(*args, stream), name, check)
+    with torch.cuda.device(device):
+        return _ret(fn(*args, stream), name, check)
 
 
 def _used_on(stream, *tensors) -> None:
@@ -540,14 +574,17 @@ def kda_decode_step(q, k, v, g, beta, state, o, N, H, dk, dv, dtype, stream=None
     return _ret(st, "kda_decode_step", check)
 
 
+@functools.lru_cache(maxsize=256)
 def kda_linear_scan_num_entries(total_tokens) -> int:
     return int(load().kda_linear_scan_num_entries(total_tokens))
 
 
+@functools.lru_cache(maxsize=256)
 def kda_linear_scan_workspace_size(total_tokens, H, d) -> int:
     return int(load().kda_linear_scan_workspace_size(total_tokens, H, d))
 
 
+@functools.lru_cache(maxsize=256)
 def kda_linear_scan_bwd_workspace_size(total_tokens, H, d) -> int:
     return int(load().kda_linear_scan_bwd_workspace_size(total_tokens, H, d))
 
@@ -555,32 +592,37 @@ def kda_linear_scan_bwd_workspace_size(total_tokens, H, d) -> int:
 def kda_linear_scan_fwd(x, g, initial_state, cu_seqlens, B, T, num_seqs, H, d, dtype, h,
                         final_state, entry_states, workspace, workspace_bytes=None, stream=None,
                         check=True) -> int:
-    _check("kda_linear_scan_fwd", dtype, typed=(x, h),
-           f32=(g, initial_state, final_state, entry_states), i32=(cu_seqlens,), raw=(workspace,))
+    code = dtype_code(dtype)
+    typed = (_TORCH_OF[code],)
+    (px, pg, ph0, pcu, ph, pf, pe, pw), dev = _args(
+        "kda_linear_scan_fwd", (x, typed), (g, _F32), (initial_state, _F32), (cu_seqlens, _I32),
+        (h, typed), (final_state, _F32), (entry_states, _F32), (workspace, _ANY))
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    return _enqueue("kda_linear_scan_fwd", x, stream, check, _p(x), _p(g), _p(initial_state),
-                    _p(cu_seqlens), B, T, num_seqs, H, d, dtype_code(dtype), _p(h),
-                    _p(final_state), _p(entry_states), _p(workspace), wb)
+    return _enqueue("kda_linear_scan_fwd", dev, stream, check, px, pg, ph0, pcu, B, T, num_seqs,
+                    H, d, code, ph, pf, pe, pw, wb)
 
 
 def kda_linear_scan_bwd(x, g, initial_state, dout, dfinal_state, entry_states, cu_seqlens, B, T,
                         num_seqs, H, d, dtype, dx, dg, dinitial_state, workspace,
                         workspace_bytes=None, stream=None, check=True) -> int:
-    _check("kda_linear_scan_bwd", dtype, typed=(x, dout, dx),
-           f32=(g, initial_state, dfinal_state, entry_states, dg, dinitial_state),
-           i32=(cu_seqlens,), raw=(workspace,))
+    code = dtype_code(dtype)
+    typed = (_TORCH_OF[code],)
+    (px, pg, ph0, pdo, pdf, pe, pcu, pdx, pdg, pdh, pw), dev = _args(
+        "kda_linear_scan_bwd", (x, typed), (g, _F32), (initial_state, _F32), (dout, typed),
+        (dfinal_state, _F32), (entry_states, _F32), (cu_seqlens, _I32), (dx, typed), (dg, _F32),
+        (dinitial_state, _F32), (workspace, _ANY))
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    return _enqueue("kda_linear_scan_bwd", x, stream, check, _p(x), _p(g), _p(initial_state),
-                    _p(dout), _p(dfinal_state), _p(entry_states), _p(cu_seqlens), B, T, num_seqs,
-                    H, d, dtype_code(dtype), _p(dx), _p(dg), _p(dinitial_state), _p(workspace),
-                    wb)
+    return _enqueue("kda_linear_scan_bwd", dev, stream, check, px, pg, ph0, pdo, pdf, pe, pcu, B,
+                    T, num_seqs, H, d, code, pdx, pdg, pdh, pw, wb)
 
 
 def kda_linear_scan_step(x, g, state_in, state_out, h, N, H, d, dtype, stream=None,
                          check=True) -> int:
-    _check("kda_linear_scan_step", dtype, typed=(x, h), f32=(g, state_in, state_out))
-    return _enqueue("kda_linear_scan_step", x, stream, check, _p(x), _p(g), _p(state_in),
-                    _p(state_out), _p(h), N, H, d, dtype_code(dtype))
+    code = dtype_code(dtype)
+    typed = (_TORCH_OF[code],)
+    (px, pg, pi, po, ph), dev = _args("kda_linear_scan_step", (x, typed), (g, _F32),
+                                      (state_in, _F32), (state_out, _F32), (h, typed))
+    return _enqueue("kda_linear_scan_step", dev, stream, check, px, pg, pi, po, ph, N, H, d, code)
 
 
 def kda_fp8_pitch(K) -> int:
@@ -589,35 +631,48 @@ def kda_fp8_pitch(K) -> int:
 
 def kda_add_rms_norm(x, residual, w, rows, D, dtype, eps, sum, y, y8, y8_scale, stream=None,
                      check=True) -> int:
-    _check("kda_add_rms_norm", dtype, typed=(x, residual, sum, y), f32=(w, y8_scale), f8=(y8,))
-    return _enqueue("kda_add_rms_norm", x, stream, check, _p(x), _p(residual), _p(w), rows, D,
-                    dtype_code(dtype), float(eps), _p(sum), _p(y), _p(y8), _p(y8_scale))
+    code = dtype_code(dtype)
+    typed = (_TORCH_OF[code],)
+    (px, pr, pw, ps, py, p8, pc), dev = _args(
+        "kda_add_rms_norm", (x, typed), (residual, typed), (w, _F32), (sum, typed), (y, typed),
+        (y8, _FP8), (y8_scale, _F32))
+    return _enqueue("kda_add_rms_norm", dev, stream, check, px, pr, pw, rows, D, code, eps, ps,
+                    py, p8, pc)
 
 
+@functools.lru_cache(maxsize=256)
 def kda_add_rms_norm_bwd_workspace_size(rows, D) -> int:
     return int(load().kda_add_rms_norm_bwd_workspace_size(rows, D))
 
 
 def kda_add_rms_norm_bwd(s, w, dy, dsum, rows, D, dtype, eps, dx, dw, workspace,
                          workspace_bytes=None, stream=None, check=True) -> int:
-    _check("kda_add_rms_norm_bwd", dtype, typed=(s, dy, dsum, dx), f32=(w, dw), raw=(workspace,))
+    code = dtype_code(dtype)
+    typed = (_TORCH_OF[code],)
+    (ps, pw, pd, pa, px, pg, pk), dev = _args(
+        "kda_add_rms_norm_bwd", (s, typed), (w, _F32), (dy, typed), (dsum, typed), (dx, typed),
+        (dw, _F32), (workspace, _ANY))
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    return _enqueue("kda_add_rms_norm_bwd", s, stream, check, _p(s), _p(w), _p(dy), _p(dsum),
-                    rows, D, dtype_code(dtype), float(eps), _p(dx), _p(dw), _p(workspace), wb)
+    return _enqueue("kda_add_rms_norm_bwd", dev, stream, check, ps, pw, pd, pa, rows, D, code,
+                    eps, px, pg, pk, wb)
 
 
 def kda_quantize_fp8(x, rows, cols, dtype, block_rows, transpose, y8, scale, stream=None,
                      check=True) -> int:
-    _check("kda_quantize_fp8", dtype, typed=(x,), f32=(scale,), f8=(y8,))
-    return _enqueue("kda_quantize_fp8", x, stream, check, _p(x), rows, cols, dtype_code(dtype),
-                    block_rows, int(bool(transpose)), _p(y8), _p(scale))
+    code = dtype_code(dtype)
+    (px, p8, pc), dev = _args("kda_quantize_fp8", (x, (_TORCH_OF[code],)), (y8, _FP8),
+                              (scale, _F32))
+    return _enqueue("kda_quantize_fp8", dev, stream, check, px, rows, cols, code, block_rows,
+                    int(bool(transpose)), p8, pc)
 
 
 def kda_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, out, stream=None,
                    check=True) -> int:
-    _check("kda_fp8_matmul", out_dtype, typed=(out,), f32=(a_scale, b_scale), f8=(a8, b8))
-    return _enqueue("kda_fp8_matmul", a8, stream, check, _p(a8), _p(a_scale), _p(b8), _p(b_scale),
-                    M, N, K, b_block_rows, dtype_code(out_dtype), _p(out))
+    code = dtype_code(out_dtype)
+    (pa, ps, pb, pt, po), dev = _args("kda_fp8_matmul", (a8, _FP8), (a_scale, _F32), (b8, _FP8),
+                                      (b_scale, _F32), (out, (_TORCH_OF[code],)))
+    return _enqueue("kda_fp8_matmul", dev, stream, check, pa, ps, pb, pt, M, N, K, b_block_rows,
+                    code, po)
 
 
 def kda_chunk_fwd_noalloc(q, k, v, g, beta, initial_state, cu_seqlens, B, T, num_seqs, H, dk,
@@ -778,9 +833,10 @@ def _scan_shape(what, x, cu_seqlens):
     return B, T, B, H, d
 
 
-def _same_shape(what, shape, **tensors):
-    for name, t in tensors.items():
-        if t is not None and tuple(t.shape) != tuple(shape):
+def _same_shape(what, shape, *named):
+    """Each of the (name, tensor or None) pairs has the given shape."""
+    for name, t in named:
+        if t is not None and t.shape != shape:
             raise ValueError(f"{what}: {name} is {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -791,8 +847,8 @@ def linear_scan(x, g, initial_state=None, cu_seqlens=None, output_final_state=Tr
     fp32; initial_state [N, H, d] fp32.  Returns (h, final_state or None), and
     the entry states linear_scan_bwd takes if output_entry_states."""
     B, T, N, H, d = _scan_shape("linear_scan", x, cu_seqlens)
-    _same_shape("linear_scan", x.shape, g=g)
-    _same_shape("linear_scan", (N, H, d), initial_state=initial_state)
+    _same_shape("linear_scan", x.shape, ("g", g))
+    _same_shape("linear_scan", (N, H, d), ("initial_state", initial_state))
     total, f32 = B * T, dict(dtype=torch.float32, device=x.device)
     h = torch.empty_like(x)
     hN = torch.empty(N, H, d, **f32) if output_final_state else None
@@ -813,12 +869,11 @@ def linear_scan_bwd(x, g, dout, initial_state=None, dfinal_state=None, cu_seqlen
     linear_scan's inputs: (dx like x, dg fp32, dinitial_state [N, H, d] fp32)."""
     B, T, N, H, d = _scan_shape("linear_scan_bwd", x, cu_seqlens)
     total, f32 = B * T, dict(dtype=torch.float32, device=x.device)
-    _same_shape("linear_scan_bwd", x.shape, g=g, dout=dout)
-    _same_shape("linear_scan_bwd", (N, H, d), initial_state=initial_state,
-                dfinal_state=dfinal_state)
-    if entry_states is not None:
-        _same_shape("linear_scan_bwd", (kda_linear_scan_num_entries(total), H, d),
-                    entry_states=entry_states)
+    _same_shape("linear_scan_bwd", x.shape, ("g", g), ("dout", dout))
+    _same_shape("linear_scan_bwd", (N, H, d), ("initial_state", initial_state),
+                ("dfinal_state", dfinal_state))
+    _same_shape("linear_scan_bwd", (kda_linear_scan_num_entries(total), H, d),
+                ("entry_states", entry_states))
     dx, dg = torch.empty_like(x), torch.empty(x.shape, **f32)
     dh0 = torch.empty(N, H, d, **f32)
     if workspace is None:
@@ -859,7 +914,8 @@ def linear_scan_step(x, g, state, h=None, state_out=None, stream=None):
     """One token of the recurrence.  x, g [N, H, d]; state [N, H, d] fp32, updated
     in place (or left alone, with the new one in state_out).  Returns h."""
     N, H, d = x.shape
-    _same_shape("linear_scan_step", x.shape, g=g, state=state, h=h, state_out=state_out)
+    _same_shape("linear_scan_step", x.shape, ("g", g), ("state", state), ("h", h),
+                ("state_out", state_out))
     made = h is None
     if made:
         h = torch.empty_like(x)
@@ -876,6 +932,10 @@ def _blocks128(n) -> int:
     return (n + 127) // 128
 
 
+def _pitch(K) -> int:   # kda_fp8_pitch
+    return (K + 15) // 16 * 16
+
+
 def add_rms_norm(x, w, residual=None, eps=1e-6, quantize=False, sum=None, stream=None):
     """RMS norm of s = x + residual over the last dimension, times w (fp32).
     Returns (s, y), or with quantize=True (s, y8, scale): y as an 8-bit matrix
@@ -883,14 +943,14 @@ def add_rms_norm(x, w, residual=None, eps=1e-6, quantize=False, sum=None, stream
     it (x or residual, to update it in place)."""
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
-    _same_shape("add_rms_norm", x.shape, residual=residual, sum=sum)
-    _same_shape("add_rms_norm", (D,), w=w)
+    _same_shape("add_rms_norm", x.shape, ("residual", residual), ("sum", sum))
+    _same_shape("add_rms_norm", (D,), ("w", w))
     s = sum
     if s is None:
         s = x if residual is None else torch.empty_like(x)
     y = y8 = scale = None
     if quantize:
-        y8 = torch.empty(rows, kda_fp8_pitch(D), dtype=torch.float8_e4m3fn, device=x.device)
+        y8 = torch.empty(rows, _pitch(D), dtype=torch.float8_e4m3fn, device=x.device)
         scale = torch.empty(_blocks128(D), rows, dtype=torch.float32, device=x.device)
     else:
         y = torch.empty_like(x)
@@ -905,8 +965,8 @@ def add_rms_norm_bwd(s, w, dy, dsum=None, eps=1e-6, workspace=None, stream=None)
     the gradient of x and of the residual."""
     D = s.shape[-1]
     rows = s.numel() // D if D else 0
-    _same_shape("add_rms_norm_bwd", s.shape, dy=dy, dsum=dsum)
-    _same_shape("add_rms_norm_bwd", (D,), w=w)
+    _same_shape("add_rms_norm_bwd", s.shape, ("dy", dy), ("dsum", dsum))
+    _same_shape("add_rms_norm_bwd", (D,), ("w", w))
     dx, dw = torch.empty_like(s), torch.empty_like(w)
     if workspace is None:
         workspace = torch.empty(kda_add_rms_norm_bwd_workspace_size(rows, D), dtype=torch.uint8,
@@ -950,7 +1010,7 @@ def quantize_fp8(x, block_rows=1, transpose=False, stream=None):
         raise ValueError(f"quantize_fp8: x is [rows, cols], got {tuple(x.shape)}")
     rows, cols = x.shape
     R, K = (cols, rows) if transpose else (rows, cols)
-    y8 = torch.empty(R, kda_fp8_pitch(K), dtype=torch.float8_e4m3fn, device=x.device)
+    y8 = torch.empty(R, _pitch(K), dtype=torch.float8_e4m3fn, device=x.device)
     scale = torch.empty(_blocks128(K), R if block_rows == 1 else _blocks128(R),
                         dtype=torch.float32, device=x.device)
     kda_quantize_fp8(x, rows, cols, x.dtype, block_rows, transpose, y8, scale, stream=stream)
@@ -966,16 +1026,17 @@ def fp8_matmul(a8, a_scale, b8, b_scale, K=None, b_block_rows=128, out_dtype=tor
     M, N = a8.shape[0], b8.shape[0]
     if K is None:
         K = a8.shape[1]
-    pitch = kda_fp8_pitch(K)
-    _same_shape("fp8_matmul", (M, pitch), a8=a8)
-    _same_shape("fp8_matmul", (N, pitch), b8=b8)
-    _same_shape("fp8_matmul", (_blocks128(K), M), a_scale=a_scale)
-    _same_shape("fp8_matmul", (_blocks128(K), N if b_block_rows == 1 else _blocks128(N)),
-                b_scale=b_scale)
+    pitch, KB = _pitch(K), _blocks128(K)
+    _same_shape("fp8_matmul", (M, pitch), ("a8", a8))
+    _same_shape("fp8_matmul", (N, pitch), ("b8", b8))
+    _same_shape("fp8_matmul", (KB, M), ("a_scale", a_scale))
+    _same_shape("fp8_matmul", (KB, N if b_block_rows == 1 else _blocks128(N)),
+                ("b_scale", b_scale))
     made = out is None
     if made:
         out = torch.empty(M, N, dtype=out_dtype, device=a8.device)
-    _same_shape("fp8_matmul", (M, N), out=out)
+    else:
+        _same_shape("fp8_matmul", (M, N), ("out", out))
     kda_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out.dtype, out, stream=stream)
     if made:
         _used_on(stream, out)
