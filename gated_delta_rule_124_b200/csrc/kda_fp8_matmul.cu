@@ -4,26 +4,23 @@
 //
 // The inner sums are e4m3 products on the tensor cores (tcgen05,
 // kind::f8f6f4, fp32 accumulation); the scales differ from block to block, so
-// every block's 128 x BM partial product leaves tensor memory and is added to
+// every block's 128 x BN partial product leaves tensor memory and is added to
 // fp32 sums in registers with its scales.  One CTA per SM walks over output
-// tiles:
+// tiles of 128 rows of A by BN rows of B:
 //   warp 0      TMA loads of both operands' blocks (128-byte rows, the swizzled
 //               K-major layout the products read), a ring of stages;
 //   warp 1      the products of a block (four of K = 32) into one of the
 //               tensor-memory buffers;
 //   warps 2, 3  the block's scales into shared memory;
 //   warps 4-11  out += scale * partial product, then the tile's output.
-// B's rows (a weight's outputs) are the 128 lanes of tensor memory and A's rows
-// (tokens) its columns: the column count BM then follows the number of tokens,
-// from 16 in a decode step to 256, and a warp writes 32 neighbouring outputs of
-// one token.  In the lanes' layout a column's scale is shared by a warp, so it
-// is read from shared memory as a broadcast; with sb per 128 rows it is one
-// number for the tile and is multiplied into the columns' scales beforehand.
-//
-// Large products are bound by the tensor cores and the partial products' way
-// out of tensor memory, small ones by reading B once.  With few tiles the K
-// blocks are split over a cluster of up to 8 CTAs, which add their partial
-// tiles through distributed shared memory in a fixed order.
+// The sums read tensor memory as 16 x 256-bit fragments: a thread holds column
+// pairs of four rows, so that a row's scale is a register and a column's is
+// read from shared memory by an eighth of the words that a row per thread would
+// take (those reads, one bank cycle per value and warp, bounded the first form
+// of this kernel: 200 us at 8192 x 4096 x 4096).  The output goes through a
+// small buffer per warp and leaves by TMA.
+// With few tiles the K blocks are split over a cluster of up to 8 CTAs, which
+// add their partial tiles through distributed shared memory in a fixed order.
 //
 // Every wait is bounded; a tile whose waits gave up is written as NaN.
 #include <cuda.h>
@@ -31,6 +28,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "kda_common.cuh"
 #include "kda_sm100.cuh"
@@ -41,31 +39,34 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 384;
-constexpr int kRowsB = 128;                       // lanes of a tile
-constexpr uint32_t kTileB = kRowsB * 128;         // bytes of B's block
+constexpr int kRowsA = 128;                       // lanes of a tile
+constexpr uint32_t kTileA = kRowsA * 128;         // bytes of A's block
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kScaleSlots = 4;
 constexpr int kMaxSplit = 8;
+constexpr int kOutBytes = 2048;                   // a warp's output buffer: 32 rows of 64 bytes
 
-template <int BM>
+template <int BN>
 struct Plan {
-    static constexpr int kBuffers = BM == 256 ? 2 : 4;       // of BM tensor-memory columns
-    static constexpr int kColumns = kBuffers * BM < 32 ? 32 : kBuffers * BM;
-    static constexpr uint32_t kStage = kTileB + BM * 128;
-    static constexpr int kStages = BM == 256 ? 4 : BM == 128 ? 6 : BM == 64 ? 8 : 9;
-    static constexpr uint32_t kSlot = (BM + kRowsB) * 4;     // column and row scales
-    static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScaleSlots * kSlot;
+    static constexpr int kBuffers = BN == 256 ? 2 : 4;       // of BN tensor-memory columns
+    static constexpr int kColumns = kBuffers * BN;
+    static constexpr uint32_t kStage = kTileA + BN * 128;
+    static constexpr int kStages = BN == 256 ? 4 : 6;
+    static constexpr uint32_t kSlot = (kRowsA + BN) * 4;     // row and column scales
+    static constexpr uint32_t kSmem =
+        1024 + kStages * kStage + 8 * kOutBytes + kScaleSlots * kSlot;
     static_assert(kSmem <= 232448 - 1024, "one CTA per SM");
-    static_assert(kStages * kStage >= BM * kRowsB * 4, "a partial tile fits the stages");
+    static constexpr int kPartPitch = BN + 8;                // floats of a partial tile's row
+    static_assert(kStages * kStage >= kPartPitch * kRowsA * 4, "a partial tile fits the stages");
 };
 
 struct MatmulArgs {
     const float* sa;  // [KB, M]
     const float* sb;  // [KB, N] or [KB, ceil(N / 128)]
     void* out;        // [M, N]
-    int M, N, KB;
-    int out_bf16;
-    int ntn, tiles, split;
+    int M, N, KB, NB; // NB: columns of sb
+    int out_bf16, tma_out;
+    int ntm, tiles, split;
 };
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
@@ -74,24 +75,38 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity, kWaitNs);
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+// 16 lanes x 32 columns: r[4 i + 2 h + j] of thread t is lane t / 4 + 8 h, column
+// 8 i + 2 (t % 4) + j.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
           "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld8(taddr, r); }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+// Waits for the loads before it; the values pass through, so that nothing reads
+// them earlier.
+__device__ __forceinline__ void tmem_wait(uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+        asm volatile("" : "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]),
+                          "+r"(a[i + 4]), "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7]));
+        asm volatile("" : "+r"(b[i]), "+r"(b[i + 1]), "+r"(b[i + 2]), "+r"(b[i + 3]),
+                          "+r"(b[i + 4]), "+r"(b[i + 5]), "+r"(b[i + 6]), "+r"(b[i + 7]));
+    }
+}
+
+// 2-D tiled store from shared memory, tracked by this thread's bulk groups.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* src, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(tmap)),
+        "r"(smem_u32(src)), "r"(c0), "r"(c1)
+        : "memory");
+}
 
 // Two fp32 values a register pair.
 __device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
@@ -111,16 +126,43 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float peer_f32(uint32_t addr, uint32_t rank) {
-    float v;
+__device__ __forceinline__ float4 peer_f32x4(uint32_t addr, uint32_t rank) {
+    float4 v;
     asm volatile(
         "{\n\t.reg .u32 p;\n\t"
-        "mapa.shared::cluster.u32 p, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [p];\n\t}"
-        : "=f"(v)
+        "mapa.shared::cluster.u32 p, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [p];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
         : "r"(addr), "r"(rank)
         : "memory");
     return v;
+}
+
+// Four neighbouring outputs from index o, `left` of the row's columns left.
+__device__ __forceinline__ void write4(const MatmulArgs& a, const float (&v)[4], size_t o,
+                                       int left) {
+    if (a.out_bf16) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + o;
+        if (a.N % 4 == 0) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(v[2], v[3]);
+            *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                        *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) out[i] = __float2bfloat16_rn(v[i]);
+        }
+    } else {
+        float* out = static_cast<float*>(a.out) + o;
+        if (a.N % 4 == 0) {
+            *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) out[i] = v[i];
+        }
+    }
 }
 
 template <int N>
@@ -132,46 +174,16 @@ __device__ __forceinline__ void set_max_regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Columns [m, m + NC) of one lane's row n of the output.  bf16: neighbouring
-// lanes swap one of two columns' values, so that each writes two outputs of one
-// token in one word (the second lane takes the odd column).
-template <int NC>
-__device__ __forceinline__ void write_columns(const MatmulArgs& a, const float (&v)[NC], int m,
-                                              int n) {
-    const size_t N = a.N;
-    if (!a.out_bf16) {
-        float* out = static_cast<float*>(a.out) + n;
-        if (n < a.N) {
-#pragma unroll
-            for (int j = 0; j < NC; ++j)
-                if (m + j < a.M) out[(size_t)(m + j) * N] = v[j];
-        }
-        return;
-    }
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-    if (a.N % 2 == 0) {
-        const int odd = threadIdx.x & 1;
-#pragma unroll
-        for (int j = 0; j < NC; j += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, v[j + 1])
-                                         : __floats2bfloat162_rn(v[j], got);
-            if (n < a.N && m + j + odd < a.M)
-                *reinterpret_cast<__nv_bfloat162*>(out + (size_t)(m + j + odd) * N + (n - odd)) = h;
-        }
-    } else if (n < a.N) {
-#pragma unroll
-        for (int j = 0; j < NC; ++j)
-            if (m + j < a.M) out[(size_t)(m + j) * N + n] = __float2bfloat16_rn(v[j]);
-    }
+__device__ __forceinline__ float half_of(uint64_t v, int j) {
+    return __uint_as_float(static_cast<uint32_t>(v >> (32 * j)));
 }
 
-template <int BM, bool kRowScales>
+template <int BN, bool kRowScales>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
-                      const MatmulArgs a) {
-    using P = Plan<BM>;
-    constexpr int ST = P::kStages, NB = P::kBuffers, NC = BM / 2;
+                      const __grid_constant__ CUtensorMap tmo, const MatmulArgs a) {
+    using P = Plan<BN>;
+    constexpr int ST = P::kStages, NB = P::kBuffers, NC = BN / 2;
     extern __shared__ uint8_t mm_smem[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[NB], tempty[NB],
         sfull[kScaleSlots], sempty[kScaleSlots];
@@ -179,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int s_fail;
 
     uint8_t* stages = mm_smem + ((1024u - (smem_u32(mm_smem) & 1023u)) & 1023u);
-    float* slots = reinterpret_cast<float*>(stages + ST * P::kStage);
+    uint8_t* out_bufs = stages + ST * P::kStage;
+    float* slots = reinterpret_cast<float*>(out_bufs + 8 * kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 1) {
@@ -208,19 +221,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s_tmem;
     volatile int* fail = &s_fail;
 
-    // this CTA's tiles and K blocks
+    // this CTA's tiles (A's rows vary fastest) and K blocks
     const int rank = blockIdx.x % a.split;
     const int kb0 = static_cast<int>((long long)rank * a.KB / a.split);
     const int kb1 = static_cast<int>((long long)(rank + 1) * a.KB / a.split);
     const int first = blockIdx.x / a.split, step = gridDim.x / a.split;
 
     if (warp < 4) {
-        if constexpr (BM == 256) set_max_regs_down<72>();
+        if constexpr (BN == 256) set_max_regs_down<72>();
         if (warp == 0) {
             if (lane == 0) {
                 int it = 0;
                 for (int tile = first; tile < a.tiles && !*fail; tile += step) {
-                    const int n0 = tile % a.ntn * kRowsB, m0 = tile / a.ntn * BM;
+                    const int m0 = tile % a.ntm * kRowsA, n0 = tile / a.ntm * BN;
                     for (int kb = kb0; kb < kb1; ++kb, ++it) {
                         const int s = it % ST;
                         if (!wait(&empty[s], ((it / ST) & 1) ^ 1)) {
@@ -229,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         uint8_t* st = stages + s * P::kStage;
                         mbar_arrive_expect_tx(&full[s], P::kStage);
-                        tma_load_2d(st, &tmb, &full[s], kb * 128, n0);
-                        tma_load_2d(st + kTileB, &tma, &full[s], kb * 128, m0);
+                        tma_load_2d(st, &tma, &full[s], kb * 128, m0);
+                        tma_load_2d(st + kTileA, &tmb, &full[s], kb * 128, n0);
                     }
                 }
                 // loads in flight land before the CTA may end (a no-op unless
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             if (lane == 0) {
-                constexpr uint32_t id = idesc_e4m3_f32(kRowsB, BM);
+                constexpr uint32_t id = idesc_e4m3_f32(kRowsA, BN);
                 int it = 0;
                 for (int tile = first; tile < a.tiles && !*fail; tile += step) {
                     for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -251,11 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sB = smem_u32(stages + s * P::kStage), sA = sB + kTileB;
+                        const uint32_t sA = smem_u32(stages + s * P::kStage), sB = sA + kTileA;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f8(tmem + b * BM, sdesc_sw128(sB + k * 32, 16, 1024),
-                                   sdesc_sw128(sA + k * 32, 16, 1024), id, k > 0);
+                            mma_f8(tmem + b * BN, sdesc_sw128(sA + k * 32, 16, 1024),
+                                   sdesc_sw128(sB + k * 32, 16, 1024), id, k > 0);
                         mma_commit(&empty[s]);
                         mma_commit(&tfull[b]);
                     }
@@ -264,56 +277,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it > 0) wait(&tfull[(it - 1) % NB], ((it - 1) / NB) & 1);
             }
         } else {
-            // scales: 64 threads; four blocks' values are requested together
-            constexpr int PER = (BM + 63) / 64;
+            // scales: 64 threads; the values of the next four blocks (across
+            // tiles) are requested before those of the last four are stored
+            constexpr int PER = kRowScales ? BN / 64 : 1, GROUP = 4;
+            struct Values {
+                float row[2], col[PER];
+            };
             const int t = threadIdx.x - 64;
-            int it = 0;
-            for (int tile = first; tile < a.tiles && !*fail; tile += step) {
-                const int nb = tile % a.ntn, n0 = nb * kRowsB, m0 = tile / a.ntn * BM;
-                for (int kb = kb0; kb < kb1; kb += 4) {
-                    float col[4][PER], row[4][2];
+            int tile = first, kb = kb0;
+            auto request = [&](Values (&v)[GROUP]) {
+                int n = 0;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const bool on = kb + u < kb1;
-                        float f = 1.f;
-                        if (!kRowScales) f = on ? a.sb[(size_t)(kb + u) * a.ntn + nb] : 0.f;
+                for (int u = 0; u < GROUP; ++u) {
+                    if (tile >= a.tiles) continue;
+                    const int m0 = tile % a.ntm * kRowsA, nt = tile / a.ntm;
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const int m = m0 + t + 64 * i;
-                            col[u][i] = on && t + 64 * i < BM && m < a.M
-                                            ? a.sa[(size_t)(kb + u) * a.M + m] * f
-                                            : 0.f;
-                        }
-                        if (kRowScales) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int n = n0 + t + 64 * i;
-                                row[u][i] =
-                                    on && n < a.N ? a.sb[(size_t)(kb + u) * a.N + n] : 0.f;
-                            }
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        const int m = m0 + t + 64 * i;
+                        v[u].row[i] = m < a.M ? a.sa[(size_t)kb * a.M + m] : 0.f;
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        if (kb + u >= kb1) break;
-                        const int i4 = it % kScaleSlots;
-                        if (!wait(&sempty[i4], ((it / kScaleSlots) & 1) ^ 1)) {
-                            *fail = 1;
-                            break;
-                        }
-                        float* slot = slots + i4 * (BM + kRowsB);
-#pragma unroll
-                        for (int i = 0; i < PER; ++i)
-                            if (t + 64 * i < BM) slot[t + 64 * i] = col[u][i];
-                        if (kRowScales) {
-                            slot[BM + t] = row[u][0];
-                            slot[BM + t + 64] = row[u][1];
-                        }
-                        mbar_arrive(&sfull[i4]);
-                        ++it;
+                    for (int i = 0; i < PER; ++i) {
+                        const int n = kRowScales ? nt * BN + t + 64 * i : nt * (BN / 128) + t;
+                        v[u].col[i] = n < a.NB && (kRowScales || t < BN / 128)
+                                          ? a.sb[(size_t)kb * a.NB + n]
+                                          : 0.f;
                     }
-                    if (*fail) break;
+                    ++n;
+                    if (++kb == kb1) {
+                        kb = kb0;
+                        tile += step;
+                    }
                 }
+                return n;
+            };
+            Values now[GROUP], next[GROUP];
+            int count = request(now), it = 0;
+            while (count > 0 && !*fail) {
+                const int more = request(next);
+#pragma unroll
+                for (int u = 0; u < GROUP; ++u) {
+                    if (u >= count) break;
+                    const int slot_of = it % kScaleSlots;
+                    if (!wait(&sempty[slot_of], ((it / kScaleSlots) & 1) ^ 1)) {
+                        *fail = 1;
+                        break;
+                    }
+                    float* slot = slots + slot_of * (kRowsA + BN);
+                    slot[t] = now[u].row[0];
+                    slot[t + 64] = now[u].row[1];
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        if (kRowScales || t < BN / 128) slot[kRowsA + t + 64 * i] = now[u].col[i];
+                    mbar_arrive(&sfull[slot_of]);
+                    ++it;
+                }
+#pragma unroll
+                for (int u = 0; u < GROUP; ++u) now[u] = next[u];
+                count = more;
             }
         }
         __syncwarp();
@@ -322,16 +343,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             cluster_sync();
         }
     } else {
-        if constexpr (BM == 256) set_max_regs_up<216>();
-        const int wg = (warp - 4) >> 2, quarter = warp & 3;
-        const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21);  // lane 32 quarter
+        if constexpr (BN == 256) set_max_regs_up<216>();
+        // this warp: lanes [32 quarter, + 32) and columns [NC wg, + NC); this
+        // thread: rows g, g + 8, g + 16, g + 24 and column pairs 8 i + 2 q
+        const int wg = (warp - 4) >> 2, quarter = warp & 3, g = lane >> 2, q = lane & 3;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21) + wg * NC;
+        uint8_t* buf = out_bufs + (warp - 4) * kOutBytes;
         int it = 0;
         for (int tile = first; tile < a.tiles; tile += step) {
-            const int n = tile % a.ntn * kRowsB + quarter * 32 + lane;
-            const int m = tile / a.ntn * BM + wg * NC;
-            uint64_t acc[NC / 2];
+            const int m = tile % a.ntm * kRowsA + quarter * 32;
+            const int n = tile / a.ntm * BN + wg * NC;
+            uint64_t acc[NC / 8][4];  // [column pair][row]
 #pragma unroll
-            for (int j = 0; j < NC / 2; ++j) acc[j] = 0ull;
+            for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) acc[j][h] = 0ull;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int b = it % NB, i4 = it % kScaleSlots;
@@ -342,77 +368,146 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const float* slot = slots + i4 * (BM + kRowsB);
-                const uint64_t rs =
-                    kRowScales ? pair(__float_as_uint(slot[BM + quarter * 32 + lane]),
-                                      __float_as_uint(slot[BM + quarter * 32 + lane]))
-                               : 0ull;
-                constexpr int CH = NC < 16 ? NC : 16;  // columns a load
+                // 32 columns of both halves of the lanes a chunk, the next
+                // chunk's loads in flight during its sums
+                const uint32_t src = tq + b * BN;
+                uint32_t r[2][2][16];
+                tmem_ld_frag(src, r[0][0]);
+                tmem_ld_frag(src + (16u << 16), r[0][1]);
+                const float* slot = slots + i4 * (kRowsA + BN);
+                uint64_t rs[4];
 #pragma unroll
-                for (int c = 0; c < NC; c += CH) {
-                    uint32_t r[CH];
-                    tmem_ld(tq + b * BM + wg * NC + c, r);
-                    tmem_wait_ld();
-                    if (c + CH == NC) {
+                for (int h = 0; h < 4; ++h) {
+                    float x = slot[quarter * 32 + g + 8 * h];
+                    if (!kRowScales) x *= slot[kRowsA + wg * NC / 128];
+                    rs[h] = pair(__float_as_uint(x), __float_as_uint(x));
+                }
+                const float* cols = slot + kRowsA + wg * NC + 2 * q;
+#pragma unroll
+                for (int c = 0; c < NC / 32; ++c) {
+                    uint32_t(&p)[2][16] = r[c & 1];
+                    tmem_wait(p[0], p[1]);
+                    if (c + 1 < NC / 32) {
+                        tmem_ld_frag(src + (c + 1) * 32, r[(c + 1) & 1][0]);
+                        tmem_ld_frag(src + (c + 1) * 32 + (16u << 16), r[(c + 1) & 1][1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&tempty[b]);
                     }
 #pragma unroll
-                    for (int j = 0; j < CH; j += 4) {
-                        const ulonglong2 s2 =
-                            *reinterpret_cast<const ulonglong2*>(slot + wg * NC + c + j);
-                        uint64_t s0 = s2.x, s1 = s2.y;
-                        if (kRowScales) {
-                            s0 = mul2(s0, rs);
-                            s1 = mul2(s1, rs);
+                    for (int i = 0; i < 4; ++i) {
+                        uint64_t cs = 0;
+                        if (kRowScales)
+                            cs = *reinterpret_cast<const uint64_t*>(cols + c * 32 + 8 * i);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const uint32_t* x = p[h >> 1] + 4 * i + 2 * (h & 1);
+                            uint64_t& d = acc[4 * c + i][h];
+                            d = fma2(pair(x[0], x[1]), kRowScales ? mul2(rs[h], cs) : rs[h], d);
                         }
-                        acc[(c + j) / 2] = fma2(pair(r[j], r[j + 1]), s0, acc[(c + j) / 2]);
-                        acc[(c + j) / 2 + 1] =
-                            fma2(pair(r[j + 2], r[j + 3]), s1, acc[(c + j) / 2 + 1]);
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sempty[i4]);
             }
-            if (a.split == 1) {
-                float v[NC];
+            if (!ok) {  // NaN instead of a sum that lacks blocks
 #pragma unroll
-                for (int j = 0; j < NC; ++j)
-                    v[j] = ok ? __uint_as_float(static_cast<uint32_t>(acc[j / 2] >> (j % 2 * 32)))
-                              : __uint_as_float(0x7FFFFFFFu);
-                write_columns<NC>(a, v, m, n);
-            } else {
-                // [column][lane]: every load of this CTA has been consumed
-                float* part = reinterpret_cast<float*>(stages);
+                for (int j = 0; j < NC / 8; ++j)
 #pragma unroll
-                for (int j = 0; j < NC; ++j)
-                    part[(wg * NC + j) * kRowsB + quarter * 32 + lane] =
-                        ok ? __uint_as_float(static_cast<uint32_t>(acc[j / 2] >> (j % 2 * 32)))
-                           : __uint_as_float(0x7FFFFFFFu);
+                    for (int h = 0; h < 4; ++h) acc[j][h] = 0x7FFFFFFF7FFFFFFFull;
+            }
+            if (a.split > 1) {
+                // [row][column], where the stages were: every load of this CTA
+                // has been consumed
+                float* part = reinterpret_cast<float*>(stages) + wg * NC + 2 * q;
+#pragma unroll
+                for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        *reinterpret_cast<uint64_t*>(
+                            part + (quarter * 32 + g + 8 * h) * P::kPartPitch + 8 * j) = acc[j][h];
+                break;
+            }
+            // 64 bytes of the 32 rows at a time: 32 bf16 or 16 fp32 columns
+            const int cols = a.out_bf16 ? 32 : 16;
+#pragma unroll
+            for (int c = 0; c < NC / 16; ++c) {
+                if (a.out_bf16 && (c & 1)) continue;
+                const int n1 = n + c * 16;
+                if (n1 >= a.N || m >= a.M) break;
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    // (16-byte chunks permuted within the rows as TMA's 64-byte
+                    // swizzle does: chunk ^ (row / 2) % 4)
+                    const int row = g + 8 * h;
+                    uint8_t* line = buf + row * 64;
+                    if (a.out_bf16) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint64_t v = acc[(2 * c + i) % (NC / 8)][h];
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(half_of(v, 0), half_of(v, 1));
+                            *reinterpret_cast<__nv_bfloat162*>(
+                                line + ((i ^ ((row >> 1) & 3)) << 4) + q * 4) = x;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint64_t*>(
+                                line + (((2 * i + (q >> 1)) ^ ((row >> 1) & 3)) << 4) + (q & 1) * 8) =
+                                acc[2 * c + i][h];
+                    }
+                }
+                if (a.tma_out) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmo, buf, n1, m);
+                        bulk_commit();
+                    }
+                } else {  // rows of `out` do not start on 16 bytes
+                    __syncwarp();
+                    for (int row = 0; row < 32 && m + row < a.M; ++row) {
+                        const size_t o = (size_t)(m + row) * a.N + n1 + lane;
+                        if (lane >= cols || n1 + lane >= a.N) continue;
+                        const int byte = lane * (a.out_bf16 ? 2 : 4);
+                        const uint8_t* x = buf + row * 64 +
+                                           (((byte >> 4) ^ ((row >> 1) & 3)) << 4) + (byte & 15);
+                        if (a.out_bf16)
+                            static_cast<__nv_bfloat16*>(a.out)[o] =
+                                *reinterpret_cast<const __nv_bfloat16*>(x);
+                        else
+                            static_cast<float*>(a.out)[o] = *reinterpret_cast<const float*>(x);
+                    }
+                    __syncwarp();
+                }
             }
             if (!ok) break;
         }
         if (a.split > 1) {
             __syncwarp();
             cluster_sync();
-            const int n0 = first % a.ntn * kRowsB, m0 = first / a.ntn * BM;
-            const int per = BM / a.split;
-            for (int e = threadIdx.x - 128; e < per * kRowsB; e += 256) {
-                const int c = rank * per + e / kRowsB, l = e % kRowsB;
-                const uint32_t addr = smem_u32(stages) + (c * kRowsB + l) * 4;
-                float v = 0.f;
-                for (int q = 0; q < a.split; ++q) v += peer_f32(addr, q);
-                if (m0 + c < a.M && n0 + l < a.N) {
-                    const size_t o = (size_t)(m0 + c) * a.N + n0 + l;
-                    if (a.out_bf16)
-                        static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
-                    else
-                        static_cast<float*>(a.out)[o] = v;
+            const int m0 = first % a.ntm * kRowsA, n0 = first / a.ntm * BN;
+            // this CTA's rows of the tile, neighbouring columns in neighbouring lanes
+            const int per = kRowsA / a.split;
+            for (int e = threadIdx.x - 128; e < per * (BN / 4); e += 256) {
+                const int l = rank * per + e / (BN / 4), c = e % (BN / 4) * 4;
+                if (m0 + l >= a.M || n0 + c >= a.N) continue;
+                const uint32_t addr = smem_u32(stages) + (l * P::kPartPitch + c) * 4;
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int p = 0; p < a.split; ++p) {
+                    const float4 x = peer_f32x4(addr, p);
+                    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
                 }
+                write4(a, v, (size_t)(m0 + l) * a.N + n0 + c, a.N - n0 - c);
             }
             __syncwarp();
             cluster_sync();  // no CTA leaves while others read its part
+        } else if (lane == 0) {
+            bulk_wait_all();
         }
     }
     tc_fence_before();
@@ -449,14 +544,32 @@ bool map_bytes(CUtensorMap* m, const void* base, int rows, int K, int box) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BM, bool kRowScales>
+// out [M, N] in boxes of 64 bytes of 32 rows, 64-byte swizzle.
+bool map_out(CUtensorMap* m, void* base, int M, int N, bool bf16) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const int es = bf16 ? 2 : 4;
+    cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    cuuint64_t strides[1] = {(cuuint64_t)N * es};
+    cuuint32_t boxes[2] = {(cuuint32_t)(64 / es), 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base,
+              dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, bool kRowScales>
 cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cudaStream_t st) {
-    using P = Plan<BM>;
-    CUtensorMap tma, tmb;
-    if (!map_bytes(&tma, a8, a.M, K, BM) || !map_bytes(&tmb, b8, a.N, K, kRowsB))
+    using P = Plan<BN>;
+    CUtensorMap tma, tmb, tmo;
+    if (!map_bytes(&tma, a8, a.M, K, kRowsA) || !map_bytes(&tmb, b8, a.N, K, BN))
         return cudaErrorInvalidValue;
+    // (rows of out start on 16 bytes)
+    a.tma_out = a.N % (a.out_bf16 ? 8 : 4) == 0;
+    if (!a.tma_out) memset(&tmo, 0, sizeof(tmo));
+    else if (!map_out(&tmo, a.out, a.M, a.N, a.out_bf16)) return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(
-        fp8_matmul_kernel<BM, kRowScales>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+        fp8_matmul_kernel<BN, kRowScales>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.split > 1 ? a.tiles * a.split : a.tiles < sms ? a.tiles : sms);
@@ -469,33 +582,20 @@ cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cu
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<BM, kRowScales>, tma, tmb, a);
+    return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<BN, kRowScales>, tma, tmb, tmo, a);
 }
 
-template <bool kRowScales>
-cudaError_t run_bm(int bm, const void* a8, const void* b8, const MatmulArgs& a, int K, int sms,
-                   cudaStream_t st) {
-    switch (bm) {
-        case 16: return run<16, kRowScales>(a8, b8, a, K, sms, st);
-        case 32: return run<32, kRowScales>(a8, b8, a, K, sms, st);
-        case 64: return run<64, kRowScales>(a8, b8, a, K, sms, st);
-        case 128: return run<128, kRowScales>(a8, b8, a, K, sms, st);
-        default: return run<256, kRowScales>(a8, b8, a, K, sms, st);
-    }
-}
-
-// Columns of a tile and the split of K.
-void choose(int M, int N, int KB, int sms, int* bm, int* split) {
-    *bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-    const long long ntn = blocks128(N);
-    while (*bm > 64 && ntn * ((M + *bm - 1) / *bm) * 2 <= sms) *bm /= 2;
-    const long long tiles = ntn * ((M + *bm - 1) / *bm);
+// Rows of B per tile and the split of K.
+void choose(int M, int N, int KB, int sms, int* bn, int* split) {
+    const long long ntm = (M + kRowsA - 1) / kRowsA;
+    *bn = ntm * ((N + 255) / 256) >= sms ? 256 : 128;
+    const long long tiles = ntm * ((N + *bn - 1) / *bn);
     int s = 1;
     while (s < kMaxSplit && tiles * s * 2 <= sms && KB >= 4 * s) s *= 2;
     *split = s;
 }
 
-cudaError_t matmul_with(int bm, int split, const void* a8, const float* a_scale, const void* b8,
+cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale, const void* b8,
                         const float* b_scale, int M, int N, int K, bool b_rows,
                         kda_dtype_t out_dt, void* out, int sms, cudaStream_t st) {
     MatmulArgs a{};
@@ -505,14 +605,16 @@ cudaError_t matmul_with(int bm, int split, const void* a8, const float* a_scale,
     a.M = M;
     a.N = N;
     a.KB = blocks128(K);
+    a.NB = b_rows ? N : blocks128(N);
     a.out_bf16 = out_dt == KDA_DTYPE_BF16;
-    a.ntn = blocks128(N);
+    a.ntm = static_cast<int>(((long long)M + kRowsA - 1) / kRowsA);
     a.split = split;
-    const long long tiles = (long long)a.ntn * (((long long)M + bm - 1) / bm);
+    const long long tiles = (long long)a.ntm * (((long long)N + bn - 1) / bn);
     if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<int>(tiles);
-    return b_rows ? run_bm<true>(bm, a8, b8, a, K, sms, st)
-                  : run_bm<false>(bm, a8, b8, a, K, sms, st);
+    if (bn == 256)
+        return b_rows ? run<256, true>(a8, b8, a, K, sms, st) : run<256, false>(a8, b8, a, K, sms, st);
+    return b_rows ? run<128, true>(a8, b8, a, K, sms, st) : run<128, false>(a8, b8, a, K, sms, st);
 }
 
 }  // namespace
@@ -527,9 +629,9 @@ cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* 
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    int bm = 0, split = 0;
-    choose(M, N, blocks128(K), sms, &bm, &split);
-    return matmul_with(bm, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, sms, st);
+    int bn = 0, split = 0;
+    choose(M, N, blocks128(K), sms, &bn, &split);
+    return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, sms, st);
 }
 
 }  // namespace kda
