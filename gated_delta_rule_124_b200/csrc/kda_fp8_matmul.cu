@@ -9,9 +9,10 @@
 // tiles of 128 rows of A by BN rows of B:
 //   warp 0      TMA loads of both operands' blocks (128-byte rows, the swizzled
 //               K-major layout the products read), a ring of stages;
-//   warp 1      the products of a block (four of K = 32) into one of the
-//               tensor-memory buffers;
-//   warps 2, 3  the block's scales into shared memory;
+//   warps 1, 2  the products of a block (four of K = 32) into one of the four
+//               tensor-memory buffers of 128 columns, in turn (the waits and
+//               hand-overs of one issuing thread take longer than a product);
+//   warp 3      the block's scales into shared memory;
 //   warps 4-11  out += scale * partial product, then the tile's output.
 // The sums read tensor memory as 16 x 256-bit fragments: a thread holds column
 // pairs of four rows, so that a row's scale is a register and a column's is
@@ -19,6 +20,11 @@
 // take (those reads, one bank cycle per value and warp, bounded the first form
 // of this kernel: 200 us at 8192 x 4096 x 4096).  The output goes through a
 // small buffer per warp and leaves by TMA.
+// A 256-column tile is two products of 128 columns, each handed to its own four
+// warps: with two buffers of 256 columns the way from a product through its
+// sums back to the buffer (a commit, a wake-up, the reads and sums, an arrival)
+// was longer than the next product, and both groups of sums competed for the
+// same issue slots at the same time (1220 cycles a block; a product takes 512).
 // With few tiles the K blocks are split over a cluster of up to 8 CTAs, which
 // add their partial tiles through distributed shared memory in a fixed order.
 //
@@ -41,15 +47,14 @@ using namespace sm100;
 constexpr int kThreads = 384;
 constexpr int kRowsA = 128;                       // lanes of a tile
 constexpr uint32_t kTileA = kRowsA * 128;         // bytes of A's block
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kScaleSlots = 4;
+constexpr int kBuffers = 4;                       // tensor-memory buffers of 128 columns
 constexpr int kMaxSplit = 8;
 constexpr int kOutBytes = 2048;                   // a warp's output buffer: 32 rows of 64 bytes
 
 template <int BN>
 struct Plan {
-    static constexpr int kBuffers = BN == 256 ? 2 : 4;       // of BN tensor-memory columns
-    static constexpr int kColumns = kBuffers * BN;
+    static constexpr int kHalves = BN / 128;                 // products of 128 columns a block
     static constexpr uint32_t kStage = kTileA + BN * 128;
     static constexpr int kStages = BN == 256 ? 4 : 6;
     static constexpr uint32_t kSlot = (kRowsA + BN) * 4;     // row and column scales
@@ -69,10 +74,15 @@ struct MatmulArgs {
     int ntm, tiles, split;
 };
 
+// Bounded wait on a phase parity (some seconds at most).  A test before the loop
+// and a plain loop of tests: the waits of the threads that issue the products
+// are mostly for phases that are complete, and with only a loop (or one with a
+// clock and a sleep in it) such a wait took 140 to 250 cycles more.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-    for (int i = 0; i < 256; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, kWaitNs);
+    if (mbar_test_wait(bar, parity)) return true;
+    for (int i = 0; i < (1 << 26); ++i)
+        if (mbar_test_wait(bar, parity)) return true;
+    return false;
 }
 
 // 16 lanes x 32 columns: r[4 i + 2 h + j] of thread t is lane t / 4 + 8 h, column
@@ -183,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                       const __grid_constant__ CUtensorMap tmo, const MatmulArgs a) {
     using P = Plan<BN>;
-    constexpr int ST = P::kStages, NB = P::kBuffers, NC = BN / 2;
+    constexpr int ST = P::kStages, NB = kBuffers, NC = BN / 2, HV = P::kHalves;
     extern __shared__ uint8_t mm_smem[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[NB], tempty[NB],
         sfull[kScaleSlots], sempty[kScaleSlots];
@@ -196,21 +206,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 1) {
-        tmem_alloc(&s_tmem, P::kColumns);
+        tmem_alloc(&s_tmem, NB * 128);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
         s_fail = 0;
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], HV);
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 8);
+            mbar_init(&tempty[i], 8 / HV);  // the warps that read it
         }
         for (int i = 0; i < kScaleSlots; ++i) {
-            mbar_init(&sfull[i], 64);
+            mbar_init(&sfull[i], 32);
             mbar_init(&sempty[i], 8);
         }
         fence_mbar_init();
@@ -230,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         if constexpr (BN == 256) set_max_regs_down<72>();
         if (warp == 0) {
-            if (lane == 0) {
+            if (elect_one()) {
                 int it = 0;
                 for (int tile = first; tile < a.tiles && !*fail; tile += step) {
                     const int m0 = tile % a.ntm * kRowsA, n0 = tile / a.ntm * BN;
@@ -251,39 +261,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int s = 0; s < ST && s < it; ++s)
                     wait(&full[s], ((it - 1 - s) / ST) & 1);
             }
-        } else if (warp == 1) {
-            if (lane == 0) {
-                constexpr uint32_t id = idesc_e4m3_f32(kRowsA, BN);
-                int it = 0;
+        } else if (warp < 3) {
+            if (elect_one()) {
+                // unit u is a block's 128 columns; this thread's: u % 2 == warp - 1
+                constexpr uint32_t id = idesc_e4m3_f32(kRowsA, 128);
+                int it = 0, last = -1;
                 for (int tile = first; tile < a.tiles && !*fail; tile += step) {
                     for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                        const int s = it % ST, b = it % NB;
-                        if (!wait(&full[s], (it / ST) & 1) ||
-                            !wait(&tempty[b], ((it / NB) & 1) ^ 1)) {
+                        const int h = HV == 2 ? warp - 1 : 0, u = it * HV + h;
+                        if (HV == 1 && (u & 1) != warp - 1) continue;
+                        const int s = it % ST, b = u % NB;
+                        if (!wait(&full[s], (it / ST) & 1)) {
+                            *fail = 1;
+                            break;
+                        }
+                        if (!wait(&tempty[b], ((u / NB) & 1) ^ 1)) {
                             *fail = 1;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sA = smem_u32(stages + s * P::kStage), sB = sA + kTileA;
+                        const uint32_t sA = smem_u32(stages + s * P::kStage);
+                        const uint32_t sB = sA + kTileA + h * 16384;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f8(tmem + b * BN, sdesc_sw128(sA + k * 32, 16, 1024),
+                            mma_f8(tmem + b * 128, sdesc_sw128(sA + k * 32, 16, 1024),
                                    sdesc_sw128(sB + k * 32, 16, 1024), id, k > 0);
-                        mma_commit(&empty[s]);
                         mma_commit(&tfull[b]);
+                        mma_commit(&empty[s]);
+                        last = u;
                     }
                 }
                 // no product is in flight when the tensor memory goes back
-                if (it > 0) wait(&tfull[(it - 1) % NB], ((it - 1) / NB) & 1);
+                if (last >= 0) wait(&tfull[last % NB], (last / NB) & 1);
             }
         } else {
-            // scales: 64 threads; the values of the next four blocks (across
-            // tiles) are requested before those of the last four are stored
-            constexpr int PER = kRowScales ? BN / 64 : 1, GROUP = 4;
+            // scales: the values of the next blocks (across tiles) are requested
+            // before those of the last ones are stored
+            constexpr int PER = kRowScales ? BN / 32 : 1, GROUP = kRowScales ? 2 : 4;
             struct Values {
-                float row[2], col[PER];
+                float row[4], col[PER];
             };
-            const int t = threadIdx.x - 64;
+            const int t = lane;
             int tile = first, kb = kb0;
             auto request = [&](Values (&v)[GROUP]) {
                 int n = 0;
@@ -292,13 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tile >= a.tiles) continue;
                     const int m0 = tile % a.ntm * kRowsA, nt = tile / a.ntm;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int m = m0 + t + 64 * i;
+                    for (int i = 0; i < 4; ++i) {
+                        const int m = m0 + t + 32 * i;
                         v[u].row[i] = m < a.M ? a.sa[(size_t)kb * a.M + m] : 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        const int n = kRowScales ? nt * BN + t + 64 * i : nt * (BN / 128) + t;
+                        const int n = kRowScales ? nt * BN + t + 32 * i : nt * (BN / 128) + t;
                         v[u].col[i] = n < a.NB && (kRowScales || t < BN / 128)
                                           ? a.sb[(size_t)kb * a.NB + n]
                                           : 0.f;
@@ -324,11 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     float* slot = slots + slot_of * (kRowsA + BN);
-                    slot[t] = now[u].row[0];
-                    slot[t + 64] = now[u].row[1];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) slot[t + 32 * i] = now[u].row[i];
 #pragma unroll
                     for (int i = 0; i < PER; ++i)
-                        if (kRowScales || t < BN / 128) slot[kRowsA + t + 64 * i] = now[u].col[i];
+                        if (kRowScales || t < BN / 128) slot[kRowsA + t + 32 * i] = now[u].col[i];
                     mbar_arrive(&sfull[slot_of]);
                     ++it;
                 }
@@ -347,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this warp: lanes [32 quarter, + 32) and columns [NC wg, + NC); this
         // thread: rows g, g + 8, g + 16, g + 24 and column pairs 8 i + 2 q
         const int wg = (warp - 4) >> 2, quarter = warp & 3, g = lane >> 2, q = lane & 3;
-        const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21) + wg * NC;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21) + (HV == 1 ? wg * NC : 0);
         uint8_t* buf = out_bufs + (warp - 4) * kOutBytes;
         int it = 0;
         for (int tile = first; tile < a.tiles; tile += step) {
@@ -360,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < 4; ++h) acc[j][h] = 0ull;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int b = it % NB, i4 = it % kScaleSlots;
-                ok = __all_sync(0xffffffffu, wait(&tfull[b], (it / NB) & 1) &&
-                                                 wait(&sfull[i4], (it / kScaleSlots) & 1));
+                const int u = HV == 1 ? it : it * HV + wg, b = u % NB, i4 = it % kScaleSlots;
+                ok = __all_sync(0xffffffffu, wait(&sfull[i4], (it / kScaleSlots) & 1) &&
+                                                 wait(&tfull[b], (u / NB) & 1));
                 if (!ok) {
                     *fail = 1;
                     break;
@@ -370,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // 32 columns of both halves of the lanes a chunk, the next
                 // chunk's loads in flight during its sums
-                const uint32_t src = tq + b * BN;
+                const uint32_t src = tq + b * 128;
                 uint32_t r[2][2][16];
                 tmem_ld_frag(src, r[0][0]);
                 tmem_ld_frag(src + (16u << 16), r[0][1]);
@@ -513,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, P::kColumns);
+    if (warp == 1) tmem_dealloc(tmem, NB * 128);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
