@@ -12,7 +12,8 @@
 //   warps 1, 2  the products of a block (four of K = 32) into one of the four
 //               tensor-memory buffers of 128 columns, in turn (the waits and
 //               hand-overs of one issuing thread take longer than a product);
-//   warp 3      the block's scales into shared memory;
+//   warp 3      the block's scales into the same stage (a product is issued when
+//               both are there, so the warps below wait for the product alone);
 //   warps 4-11  out += scale * partial product, then the tile's output.
 // The sums read tensor memory as 16 x 256-bit fragments: a thread holds column
 // pairs of four rows, so that a row's scale is a register and a column's is
@@ -47,7 +48,6 @@ using namespace sm100;
 constexpr int kThreads = 384;
 constexpr int kRowsA = 128;                       // lanes of a tile
 constexpr uint32_t kTileA = kRowsA * 128;         // bytes of A's block
-constexpr int kScaleSlots = 4;
 constexpr int kBuffers = 4;                       // tensor-memory buffers of 128 columns
 constexpr int kMaxSplit = 8;
 constexpr int kOutBytes = 2048;                   // a warp's output buffer: 32 rows of 64 bytes
@@ -59,7 +59,7 @@ struct Plan {
     static constexpr int kStages = BN == 256 ? 4 : 6;
     static constexpr uint32_t kSlot = (kRowsA + BN) * 4;     // row and column scales
     static constexpr uint32_t kSmem =
-        1024 + kStages * kStage + 8 * kOutBytes + kScaleSlots * kSlot;
+        1024 + kStages * (kStage + kSlot) + 8 * kOutBytes;
     static_assert(kSmem <= 232448 - 1024, "one CTA per SM");
     static constexpr int kPartPitch = BN + 8;                // floats of a partial tile's row
     static_assert(kStages * kStage >= kPartPitch * kRowsA * 4, "a partial tile fits the stages");
@@ -195,8 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using P = Plan<BN>;
     constexpr int ST = P::kStages, NB = kBuffers, NC = BN / 2, HV = P::kHalves;
     extern __shared__ uint8_t mm_smem[];
-    __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[NB], tempty[NB],
-        sfull[kScaleSlots], sempty[kScaleSlots];
+    __shared__ __align__(8) uint64_t full[ST], empty[ST], sempty[ST], tfull[NB], tempty[NB];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
@@ -212,16 +211,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         s_fail = 0;
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], HV);
+            mbar_init(&full[i], 1 + 32);    // the loads, the scales' warp
+            mbar_init(&empty[i], HV);       // the products
+            mbar_init(&sempty[i], 8);       // the warps that read the scales
         }
         for (int i = 0; i < NB; ++i) {
-            mbar_init(&tfull[i], 1);
+            mbar_init(&tfull[i], 2);        // the product, and its issuing thread
             mbar_init(&tempty[i], 8 / HV);  // the warps that read it
-        }
-        for (int i = 0; i < kScaleSlots; ++i) {
-            mbar_init(&sfull[i], 32);
-            mbar_init(&sempty[i], 8);
         }
         fence_mbar_init();
     }
@@ -287,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_f8(tmem + b * 128, sdesc_sw128(sA + k * 32, 16, 1024),
                                    sdesc_sw128(sB + k * 32, 16, 1024), id, k > 0);
                         mma_commit(&tfull[b]);
+                        mbar_arrive(&tfull[b]);  // (passes the scales on)
                         mma_commit(&empty[s]);
                         last = u;
                     }
@@ -336,18 +333,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < GROUP; ++u) {
                     if (u >= count) break;
-                    const int slot_of = it % kScaleSlots;
-                    if (!wait(&sempty[slot_of], ((it / kScaleSlots) & 1) ^ 1)) {
+                    const int s = it % ST;
+                    if (!wait(&sempty[s], ((it / ST) & 1) ^ 1)) {
                         *fail = 1;
                         break;
                     }
-                    float* slot = slots + slot_of * (kRowsA + BN);
+                    float* slot = slots + s * (kRowsA + BN);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) slot[t + 32 * i] = now[u].row[i];
 #pragma unroll
                     for (int i = 0; i < PER; ++i)
                         if (kRowScales || t < BN / 128) slot[kRowsA + t + 32 * i] = now[u].col[i];
-                    mbar_arrive(&sfull[slot_of]);
+                    mbar_arrive(&full[s]);
                     ++it;
                 }
 #pragma unroll
@@ -378,9 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < 4; ++h) acc[j][h] = 0ull;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int u = HV == 1 ? it : it * HV + wg, b = u % NB, i4 = it % kScaleSlots;
-                ok = __all_sync(0xffffffffu, wait(&sfull[i4], (it / kScaleSlots) & 1) &&
-                                                 wait(&tfull[b], (u / NB) & 1));
+                const int u = HV == 1 ? it : it * HV + wg, b = u % NB, s = it % ST;
+                ok = __all_sync(0xffffffffu, wait(&tfull[b], (u / NB) & 1));
                 if (!ok) {
                     *fail = 1;
                     break;
@@ -392,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t r[2][2][16];
                 tmem_ld_frag(src, r[0][0]);
                 tmem_ld_frag(src + (16u << 16), r[0][1]);
-                const float* slot = slots + i4 * (kRowsA + BN);
+                const float* slot = slots + s * (kRowsA + BN);
                 uint64_t rs[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -427,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sempty[i4]);
+                if (lane == 0) mbar_arrive(&sempty[s]);
             }
             if (!ok) {  // NaN instead of a sum that lacks blocks
 #pragma unroll
