@@ -15,12 +15,7 @@
 //   warp 3      the block's scales into the same stage (a product is issued when
 //               both are there, so the warps below wait for the product alone);
 //   warps 4-11  out += scale * partial product, then the tile's output.
-// The sums read tensor memory as 16 x 256-bit fragments: a thread holds column
-// pairs of four rows, so that a row's scale is a register and a column's is
-// read from shared memory by an eighth of the words that a row per thread would
-// take (those reads, one bank cycle per value and warp, bounded the first form
-// of this kernel: 200 us at 8192 x 4096 x 4096).  The output goes through a
-// small buffer per warp and leaves by TMA.
+// The output goes through a small buffer per warp and leaves by TMA.
 // A 256-column tile is two products of 128 columns, each handed to its own four
 // warps: with two buffers of 256 columns the way from a product through its
 // sums back to the buffer (a commit, a wake-up, the reads and sums, an arrival)
@@ -36,6 +31,9 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 #include <string.h>
+
+#include <type_traits>
+#include <utility>
 
 #include "kda_common.cuh"
 #include "kda_sm100.cuh"
@@ -85,6 +83,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
+// 32 lanes x 16 columns: thread t has lane t.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 // 16 lanes x 32 columns: r[4 i + 2 h + j] of thread t is lane t / 4 + 8 h, column
 // 8 i + 2 (t % 4) + j.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
@@ -98,15 +106,13 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
 }
 // Waits for the loads before it; the values pass through, so that nothing reads
 // them earlier.
-__device__ __forceinline__ void tmem_wait(uint32_t (&a)[16], uint32_t (&b)[16]) {
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-        asm volatile("" : "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]),
-                          "+r"(a[i + 4]), "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7]));
-        asm volatile("" : "+r"(b[i]), "+r"(b[i + 1]), "+r"(b[i + 2]), "+r"(b[i + 3]),
-                          "+r"(b[i + 4]), "+r"(b[i + 5]), "+r"(b[i + 6]), "+r"(b[i + 7]));
-    }
+    for (int i = 0; i < N; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),
+                          "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
 // 2-D tiled store from shared memory, tracked by this thread's bulk groups.
@@ -187,6 +193,159 @@ __device__ __forceinline__ void set_max_regs_up() {
 __device__ __forceinline__ float half_of(uint64_t v, int j) {
     return __uint_as_float(static_cast<uint32_t>(v >> (32 * j)));
 }
+
+// f(c) for c = 0, 1, ..., c a constant of its own type.
+template <typename F, int... c>
+__device__ __forceinline__ void for_each_chunk(F& f, std::integer_sequence<int, c...>) {
+    (f(std::integral_constant<int, c>{}), ...);
+}
+
+// A warp's part of a tile, 32 rows (the lanes of its quarter of tensor memory) by
+// NC columns of fp32 sums, in one of two layouts:
+//   RowSums:  thread t has row t, so that a block's scale is one number per
+//             thread; whole-lane loads read tensor memory at its full rate;
+//   FragSums: thread t has the column pairs 8 i + 2 (t % 4) of rows t / 4 + 8 h,
+//             for scales that differ by column: a thread needs a quarter of
+//             them (a column's scale costs a shared-memory word per warp that
+//             reads it, and whole rows' worth of them was the bound: 1100
+//             cycles a block of 256 columns), at half the rate of the loads.
+// add() adds a block: `src` its columns in tensor memory, `row` the scales of the
+// 32 rows, `col` those of the columns (RowSums: the one of the 128); `release`
+// is called when tensor memory has been read.  The loads of the next 32 columns
+// are in flight during a chunk's sums.
+// chunk() writes 64 bytes (32 bf16 or 16 fp32 columns, from column 16 c) of every
+// row to `buf`, 16-byte pieces permuted as TMA's 64-byte swizzle does.
+__device__ __forceinline__ uint32_t out_piece(int row, int piece) {
+    return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(half_of(v, 0), half_of(v, 1));
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+template <int NC>
+struct RowSums {
+    uint64_t acc[NC / 2];
+    __device__ void fill(uint64_t v) {
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j) acc[j] = v;
+    }
+    template <typename F>
+    __device__ void add(uint32_t src, const float* row, const float* col, int lane, F release) {
+        uint32_t r[2][16];
+        tmem_ld16(src, r[0]);
+        const uint32_t x = __float_as_uint(row[lane] * *col);
+        const uint64_t scale = pair(x, x);
+#pragma unroll
+        for (int c = 0; c < NC / 16; ++c) {
+            uint32_t(&p)[16] = r[c & 1];
+            tmem_wait(p);
+            if (c + 1 < NC / 16) tmem_ld16(src + (c + 1) * 16, r[(c + 1) & 1]);
+            else release();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                acc[8 * c + j] = fma2(pair(p[2 * j], p[2 * j + 1]), scale, acc[8 * c + j]);
+        }
+    }
+    // The sums as floats, the 32 rows `pitch` floats apart.
+    __device__ void partial(float* part, int pitch, int lane) const {
+#pragma unroll
+        for (int j = 0; j < NC / 2; j += 2) {
+            ulonglong2 v;
+            v.x = acc[j];
+            v.y = acc[j + 1];
+            *reinterpret_cast<ulonglong2*>(part + lane * pitch + 2 * j) = v;
+        }
+    }
+    template <int c>
+    __device__ void chunk(uint8_t* buf, int lane, bool bf16) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 v;
+            if (bf16) {
+                const uint64_t* a = acc + (8 * c + 4 * i) % (NC / 2);
+                v = make_uint4(bf16_pair(a[0]), bf16_pair(a[1]), bf16_pair(a[2]), bf16_pair(a[3]));
+            } else {
+                const uint64_t* a = acc + 8 * c + 2 * i;
+                v = make_uint4(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[0] >> 32),
+                               static_cast<uint32_t>(a[1]), static_cast<uint32_t>(a[1] >> 32));
+            }
+            *reinterpret_cast<uint4*>(buf + out_piece(lane, i)) = v;
+        }
+    }
+};
+
+template <int NC>
+struct FragSums {
+    uint64_t acc[NC / 8][4];
+    __device__ void fill(uint64_t v) {
+#pragma unroll
+        for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) acc[j][h] = v;
+    }
+    template <typename F>
+    __device__ void add(uint32_t src, const float* row, const float* col, int lane, F release) {
+        const int g = lane >> 2, q = lane & 3;
+        uint32_t r[2][2][16];
+        tmem_ld_frag(src, r[0][0]);
+        tmem_ld_frag(src + (16u << 16), r[0][1]);
+        uint64_t rs[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const uint32_t x = __float_as_uint(row[g + 8 * h]);
+            rs[h] = pair(x, x);
+        }
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) {
+            uint32_t(&p)[2][16] = r[c & 1];
+            tmem_wait(p[0]);
+            tmem_wait(p[1]);
+            if (c + 1 < NC / 32) {
+                tmem_ld_frag(src + (c + 1) * 32, r[(c + 1) & 1][0]);
+                tmem_ld_frag(src + (c + 1) * 32 + (16u << 16), r[(c + 1) & 1][1]);
+            } else {
+                release();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t cs = *reinterpret_cast<const uint64_t*>(col + c * 32 + 8 * i + 2 * q);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t* x = p[h >> 1] + 4 * i + 2 * (h & 1);
+                    acc[4 * c + i][h] = fma2(pair(x[0], x[1]), mul2(rs[h], cs), acc[4 * c + i][h]);
+                }
+            }
+        }
+    }
+    __device__ void partial(float* part, int pitch, int lane) const {
+        part += (lane >> 2) * pitch + 2 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                *reinterpret_cast<uint64_t*>(part + 8 * h * pitch + 8 * j) = acc[j][h];
+    }
+    template <int c>
+    __device__ void chunk(uint8_t* buf, int lane, bool bf16) const {
+        const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const int row = g + 8 * h;
+            if (bf16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint32_t*>(buf + out_piece(row, i) + q * 4) =
+                        bf16_pair(acc[(2 * c + i) % (NC / 8)][h]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint64_t*>(buf + out_piece(row, 2 * i + (q >> 1)) +
+                                                 (q & 1) * 8) = acc[2 * c + i][h];
+            }
+        }
+    }
+};
 
 template <int BN, bool kRowScales>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -359,20 +518,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         if constexpr (BN == 256) set_max_regs_up<216>();
-        // this warp: lanes [32 quarter, + 32) and columns [NC wg, + NC); this
-        // thread: rows g, g + 8, g + 16, g + 24 and column pairs 8 i + 2 q
-        const int wg = (warp - 4) >> 2, quarter = warp & 3, g = lane >> 2, q = lane & 3;
+        // this warp: lanes [32 quarter, + 32) and columns [NC wg, + NC)
+        const int wg = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21) + (HV == 1 ? wg * NC : 0);
         uint8_t* buf = out_bufs + (warp - 4) * kOutBytes;
         int it = 0;
         for (int tile = first; tile < a.tiles; tile += step) {
             const int m = tile % a.ntm * kRowsA + quarter * 32;
             const int n = tile / a.ntm * BN + wg * NC;
-            uint64_t acc[NC / 8][4];  // [column pair][row]
-#pragma unroll
-            for (int j = 0; j < NC / 8; ++j)
-#pragma unroll
-                for (int h = 0; h < 4; ++h) acc[j][h] = 0ull;
+            typename std::conditional<kRowScales, FragSums<NC>, RowSums<NC>>::type sums;
+            sums.fill(0ull);
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int u = HV == 1 ? it : it * HV + wg, b = u % NB, s = it % ST;
@@ -382,98 +537,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                // 32 columns of both halves of the lanes a chunk, the next
-                // chunk's loads in flight during its sums
-                const uint32_t src = tq + b * 128;
-                uint32_t r[2][2][16];
-                tmem_ld_frag(src, r[0][0]);
-                tmem_ld_frag(src + (16u << 16), r[0][1]);
                 const float* slot = slots + s * (kRowsA + BN);
-                uint64_t rs[4];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float x = slot[quarter * 32 + g + 8 * h];
-                    if (!kRowScales) x *= slot[kRowsA + wg * NC / 128];
-                    rs[h] = pair(__float_as_uint(x), __float_as_uint(x));
-                }
-                const float* cols = slot + kRowsA + wg * NC + 2 * q;
-#pragma unroll
-                for (int c = 0; c < NC / 32; ++c) {
-                    uint32_t(&p)[2][16] = r[c & 1];
-                    tmem_wait(p[0], p[1]);
-                    if (c + 1 < NC / 32) {
-                        tmem_ld_frag(src + (c + 1) * 32, r[(c + 1) & 1][0]);
-                        tmem_ld_frag(src + (c + 1) * 32 + (16u << 16), r[(c + 1) & 1][1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[b]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint64_t cs = 0;
-                        if (kRowScales)
-                            cs = *reinterpret_cast<const uint64_t*>(cols + c * 32 + 8 * i);
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const uint32_t* x = p[h >> 1] + 4 * i + 2 * (h & 1);
-                            uint64_t& d = acc[4 * c + i][h];
-                            d = fma2(pair(x[0], x[1]), kRowScales ? mul2(rs[h], cs) : rs[h], d);
-                        }
-                    }
-                }
+                sums.add(tq + b * 128, slot + quarter * 32,
+                         slot + kRowsA + (kRowScales ? wg * NC : wg * NC / 128), lane, [&] {
+                             tc_fence_before();
+                             __syncwarp();
+                             if (lane == 0) mbar_arrive(&tempty[b]);
+                         });
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sempty[s]);
             }
-            if (!ok) {  // NaN instead of a sum that lacks blocks
-#pragma unroll
-                for (int j = 0; j < NC / 8; ++j)
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) acc[j][h] = 0x7FFFFFFF7FFFFFFFull;
-            }
+            // NaN instead of a sum that lacks blocks
+            if (!ok) sums.fill(0x7FFFFFFF7FFFFFFFull);
             if (a.split > 1) {
                 // [row][column], where the stages were: every load of this CTA
                 // has been consumed
-                float* part = reinterpret_cast<float*>(stages) + wg * NC + 2 * q;
-#pragma unroll
-                for (int j = 0; j < NC / 8; ++j)
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        *reinterpret_cast<uint64_t*>(
-                            part + (quarter * 32 + g + 8 * h) * P::kPartPitch + 8 * j) = acc[j][h];
+                sums.partial(reinterpret_cast<float*>(stages) + quarter * 32 * P::kPartPitch + wg * NC,
+                             P::kPartPitch, lane);
                 break;
             }
-            // 64 bytes of the 32 rows at a time: 32 bf16 or 16 fp32 columns
-            const int cols = a.out_bf16 ? 32 : 16;
-#pragma unroll
-            for (int c = 0; c < NC / 16; ++c) {
-                if (a.out_bf16 && (c & 1)) continue;
+            const int cols = a.out_bf16 ? 32 : 16;  // 64 bytes
+            auto write = [&](auto chunk) {
+                constexpr int c = decltype(chunk)::value;
                 const int n1 = n + c * 16;
-                if (n1 >= a.N || m >= a.M) break;
+                if ((a.out_bf16 && (c & 1)) || n1 >= a.N || m >= a.M) return;
                 if (lane == 0) bulk_wait_read();
                 __syncwarp();
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    // (16-byte chunks permuted within the rows as TMA's 64-byte
-                    // swizzle does: chunk ^ (row / 2) % 4)
-                    const int row = g + 8 * h;
-                    uint8_t* line = buf + row * 64;
-                    if (a.out_bf16) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint64_t v = acc[(2 * c + i) % (NC / 8)][h];
-                            const __nv_bfloat162 x = __floats2bfloat162_rn(half_of(v, 0), half_of(v, 1));
-                            *reinterpret_cast<__nv_bfloat162*>(
-                                line + ((i ^ ((row >> 1) & 3)) << 4) + q * 4) = x;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint64_t*>(
-                                line + (((2 * i + (q >> 1)) ^ ((row >> 1) & 3)) << 4) + (q & 1) * 8) =
-                                acc[2 * c + i][h];
-                    }
-                }
+                sums.template chunk<c>(buf, lane, a.out_bf16);
                 if (a.tma_out) {
                     fence_async_smem();
                     __syncwarp();
@@ -487,8 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const size_t o = (size_t)(m + row) * a.N + n1 + lane;
                         if (lane >= cols || n1 + lane >= a.N) continue;
                         const int byte = lane * (a.out_bf16 ? 2 : 4);
-                        const uint8_t* x = buf + row * 64 +
-                                           (((byte >> 4) ^ ((row >> 1) & 3)) << 4) + (byte & 15);
+                        const uint8_t* x = buf + out_piece(row, byte >> 4) + (byte & 15);
                         if (a.out_bf16)
                             static_cast<__nv_bfloat16*>(a.out)[o] =
                                 *reinterpret_cast<const __nv_bfloat16*>(x);
@@ -497,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-            }
+            };
+            for_each_chunk(write, std::make_integer_sequence<int, NC / 16>{});
             if (!ok) break;
         }
         if (a.split > 1) {
