@@ -15,7 +15,9 @@
 //   warp 3      the block's scales into the same stage (a product is issued when
 //               both are there, so the warps below wait for the product alone);
 //   warps 4-11  out += scale * partial product, then the tile's output.
-// The output goes through a small buffer per warp and leaves by TMA.
+// The output is stored from registers, whole 32-byte sectors where a thread has a
+// row (through shared memory and TMA it took 2900 cycles a tile, the time of five
+// blocks' products, in which the sums waited for their buffers).
 // A 256-column tile is two products of 128 columns, each handed to its own four
 // warps: with two buffers of 256 columns the way from a product through its
 // sums back to the buffer (a commit, a wake-up, the reads and sums, an arrival)
@@ -30,10 +32,8 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <stdint.h>
-#include <string.h>
 
 #include <type_traits>
-#include <utility>
 
 #include "kda_common.cuh"
 #include "kda_sm100.cuh"
@@ -48,7 +48,6 @@ constexpr int kRowsA = 128;                       // lanes of a tile
 constexpr uint32_t kTileA = kRowsA * 128;         // bytes of A's block
 constexpr int kBuffers = 4;                       // tensor-memory buffers of 128 columns
 constexpr int kMaxSplit = 8;
-constexpr int kOutBytes = 2048;                   // a warp's output buffer: 32 rows of 64 bytes
 
 template <int BN>
 struct Plan {
@@ -57,7 +56,7 @@ struct Plan {
     static constexpr int kStages = BN == 256 ? 4 : 6;
     static constexpr uint32_t kSlot = (kRowsA + BN) * 4;     // row and column scales
     static constexpr uint32_t kSmem =
-        1024 + kStages * (kStage + kSlot) + 8 * kOutBytes;
+        1024 + kStages * (kStage + kSlot);
     static_assert(kSmem <= 232448 - 1024, "one CTA per SM");
     static constexpr int kPartPitch = BN + 8;                // floats of a partial tile's row
     static_assert(kStages * kStage >= kPartPitch * kRowsA * 4, "a partial tile fits the stages");
@@ -68,7 +67,7 @@ struct MatmulArgs {
     const float* sb;  // [KB, N] or [KB, ceil(N / 128)]
     void* out;        // [M, N]
     int M, N, KB, NB; // NB: columns of sb
-    int out_bf16, tma_out;
+    int out_bf16;
     int ntm, tiles, split;
 };
 
@@ -113,15 +112,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
     for (int i = 0; i < N; i += 8)
         asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),
                           "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
-}
-
-// 2-D tiled store from shared memory, tracked by this thread's bulk groups.
-__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* src, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-            reinterpret_cast<uint64_t>(tmap)),
-        "r"(smem_u32(src)), "r"(c0), "r"(c1)
-        : "memory");
 }
 
 // Two fp32 values a register pair.
@@ -194,10 +184,14 @@ __device__ __forceinline__ float half_of(uint64_t v, int j) {
     return __uint_as_float(static_cast<uint32_t>(v >> (32 * j)));
 }
 
-// f(c) for c = 0, 1, ..., c a constant of its own type.
-template <typename F, int... c>
-__device__ __forceinline__ void for_each_chunk(F& f, std::integer_sequence<int, c...>) {
-    (f(std::integral_constant<int, c>{}), ...);
+__device__ __forceinline__ void store32(void* p, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 words(uint64_t a, uint64_t b) {
+    return make_uint4(static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32),
+                      static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32));
 }
 
 // A warp's part of a tile, 32 rows (the lanes of its quarter of tensor memory) by
@@ -213,11 +207,7 @@ __device__ __forceinline__ void for_each_chunk(F& f, std::integer_sequence<int, 
 // 32 rows, `col` those of the columns (RowSums: the one of the 128); `release`
 // is called when tensor memory has been read.  The loads of the next 32 columns
 // are in flight during a chunk's sums.
-// chunk() writes 64 bytes (32 bf16 or 16 fp32 columns, from column 16 c) of every
-// row to `buf`, 16-byte pieces permuted as TMA's 64-byte swizzle does.
-__device__ __forceinline__ uint32_t out_piece(int row, int piece) {
-    return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-}
+// store() writes the part, whose first row and column are m and n, to the output.
 __device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(half_of(v, 0), half_of(v, 1));
     return *reinterpret_cast<const uint32_t*>(&x);
@@ -257,20 +247,40 @@ struct RowSums {
             *reinterpret_cast<ulonglong2*>(part + lane * pitch + 2 * j) = v;
         }
     }
-    template <int c>
-    __device__ void chunk(uint8_t* buf, int lane, bool bf16) const {
+    __device__ void store(const MatmulArgs& a, int m, int n, int lane) const {
+        if (m + lane >= a.M) return;
+        const size_t o = (size_t)(m + lane) * a.N + n;
+        const int left = a.N - n;  // columns of the output from n on
+        if (a.out_bf16) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + o;
+            if (a.N % 16 == 0) {  // rows, and 16 columns, start on 32 bytes
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint4 v;
-            if (bf16) {
-                const uint64_t* a = acc + (8 * c + 4 * i) % (NC / 2);
-                v = make_uint4(bf16_pair(a[0]), bf16_pair(a[1]), bf16_pair(a[2]), bf16_pair(a[3]));
+                for (int j = 0; j < NC / 16; ++j) {
+                    if (16 * j >= left) break;
+                    const uint64_t* v = acc + 8 * j;
+                    store32(out + 16 * j,
+                            make_uint4(bf16_pair(v[0]), bf16_pair(v[1]), bf16_pair(v[2]), bf16_pair(v[3])),
+                            make_uint4(bf16_pair(v[4]), bf16_pair(v[5]), bf16_pair(v[6]), bf16_pair(v[7])));
+                }
             } else {
-                const uint64_t* a = acc + 8 * c + 2 * i;
-                v = make_uint4(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[0] >> 32),
-                               static_cast<uint32_t>(a[1]), static_cast<uint32_t>(a[1] >> 32));
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+                    if (j < left) out[j] = __float2bfloat16_rn(half_of(acc[j / 2], j % 2));
             }
-            *reinterpret_cast<uint4*>(buf + out_piece(lane, i)) = v;
+        } else {
+            float* out = static_cast<float*>(a.out) + o;
+            if (a.N % 8 == 0) {
+#pragma unroll
+                for (int j = 0; j < NC / 8; ++j) {
+                    if (8 * j >= left) break;
+                    const uint64_t* v = acc + 4 * j;
+                    store32(out + 8 * j, words(v[0], v[1]), words(v[2], v[3]));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+                    if (j < left) out[j] = half_of(acc[j / 2], j % 2);
+            }
         }
     }
 };
@@ -326,22 +336,31 @@ struct FragSums {
             for (int h = 0; h < 4; ++h)
                 *reinterpret_cast<uint64_t*>(part + 8 * h * pitch + 8 * j) = acc[j][h];
     }
-    template <int c>
-    __device__ void chunk(uint8_t* buf, int lane, bool bf16) const {
-        const int g = lane >> 2, q = lane & 3;
+    __device__ void store(const MatmulArgs& a, int m, int n, int lane) const {
+        n += 2 * (lane & 3);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            const int row = g + 8 * h;
-            if (bf16) {
+            const int row = m + (lane >> 2) + 8 * h;
+            if (row >= a.M) break;
+            const size_t o = (size_t)row * a.N + n;
+            const int left = a.N - n;
+            __nv_bfloat16* half = static_cast<__nv_bfloat16*>(a.out) + o;
+            float* full = static_cast<float*>(a.out) + o;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint32_t*>(buf + out_piece(row, i) + q * 4) =
-                        bf16_pair(acc[(2 * c + i) % (NC / 8)][h]);
-            } else {
+            for (int j = 0; j < NC / 8; ++j) {
+                if (8 * j >= left) break;
+                const uint64_t v = acc[j][h];
+                if (a.N % 2 == 0) {  // pairs start on 4 or 8 bytes
+                    if (a.out_bf16) *reinterpret_cast<uint32_t*>(half + 8 * j) = bf16_pair(v);
+                    else *reinterpret_cast<uint64_t*>(full + 8 * j) = v;
+                    continue;
+                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint64_t*>(buf + out_piece(row, 2 * i + (q >> 1)) +
-                                                 (q & 1) * 8) = acc[2 * c + i][h];
+                for (int e = 0; e < 2; ++e) {
+                    if (8 * j + e >= left) break;
+                    if (a.out_bf16) half[8 * j + e] = __float2bfloat16_rn(half_of(v, e));
+                    else full[8 * j + e] = half_of(v, e);
+                }
             }
         }
     }
@@ -350,7 +369,7 @@ struct FragSums {
 template <int BN, bool kRowScales>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
-                      const __grid_constant__ CUtensorMap tmo, const MatmulArgs a) {
+                      const MatmulArgs a) {
     using P = Plan<BN>;
     constexpr int ST = P::kStages, NB = kBuffers, NC = BN / 2, HV = P::kHalves;
     extern __shared__ uint8_t mm_smem[];
@@ -359,8 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int s_fail;
 
     uint8_t* stages = mm_smem + ((1024u - (smem_u32(mm_smem) & 1023u)) & 1023u);
-    uint8_t* out_bufs = stages + ST * P::kStage;
-    float* slots = reinterpret_cast<float*>(out_bufs + 8 * kOutBytes);
+    float* slots = reinterpret_cast<float*>(stages + ST * P::kStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 1) {
@@ -521,7 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this warp: lanes [32 quarter, + 32) and columns [NC wg, + NC)
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21) + (HV == 1 ? wg * NC : 0);
-        uint8_t* buf = out_bufs + (warp - 4) * kOutBytes;
         int it = 0;
         for (int tile = first; tile < a.tiles; tile += step) {
             const int m = tile % a.ntm * kRowsA + quarter * 32;
@@ -556,38 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              P::kPartPitch, lane);
                 break;
             }
-            const int cols = a.out_bf16 ? 32 : 16;  // 64 bytes
-            auto write = [&](auto chunk) {
-                constexpr int c = decltype(chunk)::value;
-                const int n1 = n + c * 16;
-                if ((a.out_bf16 && (c & 1)) || n1 >= a.N || m >= a.M) return;
-                if (lane == 0) bulk_wait_read();
-                __syncwarp();
-                sums.template chunk<c>(buf, lane, a.out_bf16);
-                if (a.tma_out) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmo, buf, n1, m);
-                        bulk_commit();
-                    }
-                } else {  // rows of `out` do not start on 16 bytes
-                    __syncwarp();
-                    for (int row = 0; row < 32 && m + row < a.M; ++row) {
-                        const size_t o = (size_t)(m + row) * a.N + n1 + lane;
-                        if (lane >= cols || n1 + lane >= a.N) continue;
-                        const int byte = lane * (a.out_bf16 ? 2 : 4);
-                        const uint8_t* x = buf + out_piece(row, byte >> 4) + (byte & 15);
-                        if (a.out_bf16)
-                            static_cast<__nv_bfloat16*>(a.out)[o] =
-                                *reinterpret_cast<const __nv_bfloat16*>(x);
-                        else
-                            static_cast<float*>(a.out)[o] = *reinterpret_cast<const float*>(x);
-                    }
-                    __syncwarp();
-                }
-            };
-            for_each_chunk(write, std::make_integer_sequence<int, NC / 16>{});
+            sums.store(a, m, n, lane);
             if (!ok) break;
         }
         if (a.split > 1) {
@@ -610,8 +596,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             cluster_sync();  // no CTA leaves while others read its part
-        } else if (lane == 0) {
-            bulk_wait_all();
         }
     }
     tc_fence_before();
@@ -648,30 +632,12 @@ bool map_bytes(CUtensorMap* m, const void* base, int rows, int K, int box) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// out [M, N] in boxes of 64 bytes of 32 rows, 64-byte swizzle.
-bool map_out(CUtensorMap* m, void* base, int M, int N, bool bf16) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const int es = bf16 ? 2 : 4;
-    cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
-    cuuint64_t strides[1] = {(cuuint64_t)N * es};
-    cuuint32_t boxes[2] = {(cuuint32_t)(64 / es), 32};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base,
-              dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int BN, bool kRowScales>
 cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cudaStream_t st) {
     using P = Plan<BN>;
-    CUtensorMap tma, tmb, tmo;
+    CUtensorMap tma, tmb;
     if (!map_bytes(&tma, a8, a.M, K, kRowsA) || !map_bytes(&tmb, b8, a.N, K, BN))
         return cudaErrorInvalidValue;
-    // (rows of out start on 16 bytes)
-    a.tma_out = a.N % (a.out_bf16 ? 8 : 4) == 0;
-    if (!a.tma_out) memset(&tmo, 0, sizeof(tmo));
-    else if (!map_out(&tmo, a.out, a.M, a.N, a.out_bf16)) return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(
         fp8_matmul_kernel<BN, kRowScales>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
     if (e != cudaSuccess) return e;
@@ -686,7 +652,7 @@ cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cu
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<BN, kRowScales>, tma, tmb, tmo, a);
+    return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<BN, kRowScales>, tma, tmb, a);
 }
 
 // Rows of B per tile and the split of K.
