@@ -33,6 +33,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "kda_common.cuh"
@@ -569,8 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.split > 1) {
                 // [row][column], where the stages were: every load of this CTA
                 // has been consumed
-                sums.partial(reinterpret_cast<float*>(stages) + quarter * 32 * P::kPartPitch + wg * NC,
-                             P::kPartPitch, lane);
+                if (m < a.M)
+                    sums.partial(reinterpret_cast<float*>(stages) + quarter * 32 * P::kPartPitch +
+                                     wg * NC,
+                                 P::kPartPitch, lane);
                 break;
             }
             sums.store(a, m, n, lane);
@@ -580,11 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             cluster_sync();
             const int m0 = first % a.ntm * kRowsA, n0 = first / a.ntm * BN;
-            // this CTA's rows of the tile, neighbouring columns in neighbouring lanes
-            const int per = kRowsA / a.split;
-            for (int e = threadIdx.x - 128; e < per * (BN / 4); e += 256) {
-                const int l = rank * per + e / (BN / 4), c = e % (BN / 4) * 4;
-                if (m0 + l >= a.M || n0 + c >= a.N) continue;
+            // this CTA's share of the tile, neighbouring columns in neighbouring lanes
+            const int all = min(kRowsA, a.M - m0) * (BN / 4);
+            const int e0 = all * rank / a.split, e1 = all * (rank + 1) / a.split;
+            for (int e = e0 + threadIdx.x - 128; e < e1; e += 256) {
+                const int l = e / (BN / 4), c = e % (BN / 4) * 4;
+                if (n0 + c >= a.N) continue;
                 const uint32_t addr = smem_u32(stages) + (l * P::kPartPitch + c) * 4;
                 float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -655,14 +659,29 @@ cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cu
     return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<BN, kRowScales>, tma, tmb, a);
 }
 
-// Rows of B per tile and the split of K.
-void choose(int M, int N, int KB, int sms, int* bn, int* split) {
-    const long long ntm = (M + kRowsA - 1) / kRowsA;
-    *bn = ntm * ((N + 255) / 256) >= sms ? 256 : 128;
-    const long long tiles = ntm * ((N + *bn - 1) / *bn);
-    int s = 1;
-    while (s < kMaxSplit && tiles * s * 2 <= sms && KB >= 4 * s) s *= 2;
-    *split = s;
+// Rows of B per tile and the split of K: the pair with the least time by a model
+// of B200 measurements (us): a block takes 0.39 with 128 rows and 0.54 with 256
+// (all SMs busy), joining a cluster's partial tiles 4 and 7.  K = 4096, N = 4096,
+// measured for 128, 256, 512, 1024 and 8192 rows of A: 128 rows of B split 4 ways
+// 12.0 (16.7 unsplit), 2 ways 15.2 (16.9), unsplit 17.6; 256 rows unsplit 22.3
+// (29.6 with 128) and 134 (174).  With a scale per row of B 0.53 and 0.83
+// (4096 x 4096 x 4099: 110 with 256 rows, 124 with 128).
+void choose(int M, int N, int KB, bool b_rows, int sms, int* bn, int* split) {
+    double best = 0.;
+    for (int n = 128; n <= 256; n += 128) {
+        const double block = b_rows ? (n == 128 ? 0.53 : 0.83) : (n == 128 ? 0.39 : 0.54);
+        const double join = n == 128 ? 4. : 7.;
+        const double tiles = ((M + kRowsA - 1) / kRowsA) * (double)((N + n - 1) / n);
+        for (int s = 1; s <= kMaxSplit && s <= KB; s *= 2) {
+            const double rounds = std::ceil(tiles / (sms / s));
+            const double t = rounds * ((KB + s - 1) / s * block + (s > 1 ? join : 0.));
+            if (best == 0. || t < best) {
+                best = t;
+                *bn = n;
+                *split = s;
+            }
+        }
+    }
 }
 
 cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale, const void* b8,
@@ -699,8 +718,14 @@ cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* 
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    // few rows: the kernel without stages, while it takes a round or two
+    // (4096 x 4096, 8 and 16 rows of A: 6.2 and 9.8 us against 10.2 and 10.3 here;
+    // 12288 x 4096: 15.0 and 24.7 against 19.3)
+    const long long rounds = ((long long)N + 32 * sms - 1) / (32 * sms) * ((K + 4095) / 4096);
+    if (M <= 8 ? K <= 8192 : M <= 16 && rounds <= 2)
+        return launch_fp8_small(a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, st);
     int bn = 0, split = 0;
-    choose(M, N, blocks128(K), sms, &bn, &split);
+    choose(M, N, blocks128(K), b_rows, sms, &bn, &split);
     return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, sms, st);
 }
 
