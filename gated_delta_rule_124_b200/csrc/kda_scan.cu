@@ -51,9 +51,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kR = 8;                  // rows of a warp
-constexpr int kRows = kR * kWarps;     // rows of a tile
-static_assert(kRows == kScanRows, "the entry states are those of the tiles");
+// A warp has R rows of a tile and a lane VEC channels; a tile has 8 R rows, a
+// multiple of the kScanRows between entry states.
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // NaN patterns no sum of logarithms has
 constexpr uint32_t kExit = 0xFFFFFFFEu;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -76,7 +75,7 @@ struct ScanArgs {
     uint32_t* status;
     uint32_t* ticket;       // starts at 0xFFFFFFFF; NULL: one tile per channel block
     uint64_t* words;        // [tiles, C]
-    int tiles, ctiles;
+    int tiles, ctiles;      // of the launched kernel's size
 };
 
 // Four channels (VEC = 4) or one (VEC = 1) of a row; fp32 or bf16.
@@ -200,13 +199,15 @@ __device__ float look_back(const uint64_t* words, size_t C, int first, int step,
 // Where the tile's sequences begin and end: first_of[r] = the sequence whose first
 // token is row r, last_of[r] = the one whose last token it is, -1 elsewhere.
 // Reads of cu stay inside [0, N] and writes inside the tile whatever cu holds.
+template <int kRows>
 struct Bounds {
     int first_of[kRows], last_of[kRows];
     int lo;      // the last sequence whose first token is at or before the tile
     int plain;   // the tile lies inside one sequence, which goes on beyond both ends
 };
 // By every thread of the CTA; ends with a barrier.
-__device__ __forceinline__ void find_bounds(const ScanArgs& a, int t0, Bounds& s) {
+template <int kRows>
+__device__ __forceinline__ void find_bounds(const ScanArgs& a, int t0, Bounds<kRows>& s) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         int lo = 0;
@@ -284,14 +285,14 @@ __device__ __forceinline__ int next_tile(const ScanArgs& a) {
 // A warp's rows of a tile in registers.  Lanes beyond the last channel load the
 // last ones again (they store nothing); rows beyond the last token hold zeros,
 // which change no state.
-template <int VEC, typename U>
-__device__ __forceinline__ void load_rows(Raw<VEC, U> (&v)[kR], const U* p, size_t C, int rows) {
-    if (rows >= kR) {
+template <int VEC, int R, typename U>
+__device__ __forceinline__ void load_rows(Raw<VEC, U> (&v)[R], const U* p, size_t C, int rows) {
+    if (rows >= R) {
 #pragma unroll
-        for (int r = 0; r < kR; ++r) v[r].load(p + r * C);
+        for (int r = 0; r < R; ++r) v[r].load(p + r * C);
     } else {
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
+        for (int r = 0; r < R; ++r) {
             v[r].zero();
             if (r < rows) v[r].load(p + r * C);
         }
@@ -339,26 +340,26 @@ struct Maps {
 };
 
 // kBounds: sequences begin or end in the tile, or the tokens do.
-template <int VEC, typename T, bool kBounds>
+template <int VEC, int R, typename T, bool kBounds>
 __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Maps<VEC>& s_maps,
-                                         const Bounds& s_bounds, const Raw<VEC, T> (&xr)[kR],
-                                         const Raw<VEC, float> (&gr)[kR], int c, bool mine) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = tile * kRows;
+                                         const Bounds<8 * R>& s_bounds, const Raw<VEC, T> (&xr)[R],
+                                         const Raw<VEC, float> (&gr)[R], int c, bool mine) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = tile * 8 * R;
     const size_t C = a.C;
     // the map of this warp's rows
-    float al[kR][VEC];
+    float al[R][VEC];
     {
         float G[VEC], b[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
+        for (int r = 0; r < R; ++r) {
             float gv[VEC], xv[VEC];
             gr[r].get(gv);
             xr[r].get(xv);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) al[r][j] = gate(gv[j], G[j]);
-            const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+            const int first = kBounds ? s_bounds.first_of[w * R + r] : -1;
             if (kBounds && first >= 0) {
                 state_of<VEC>(a.h0, first, C, c, b);
 #pragma unroll
@@ -397,7 +398,15 @@ __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Ma
             }
         }
         s_maps.template walk<false, true>(ch, h);
-        if (a.entry) a.entry[(size_t)tile * C + c0 + ch] = h;
+        if (a.entry) {  // the states before rows 0, kScanRows, ... of the tile
+            constexpr int W = kScanRows / R < 1 ? 1 : kScanRows / R;
+            const int n0 = t0 / kScanRows, n1 = (a.total - 1) / kScanRows;
+#pragma unroll
+            for (int i = 0; i < kWarps; i += W) {
+                const int n = n0 + i * R / kScanRows;
+                if (i == 0 || n <= n1) a.entry[(size_t)n * C + c0 + ch] = s_maps.b[i][ch];
+            }
+        }
     }
     if (!a.h && !a.final_state) return;
     __syncthreads();
@@ -407,18 +416,18 @@ __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Ma
     float h[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) h[j] = s_maps.b[w][lane * VEC + j];
-    T* out = static_cast<T*>(a.h) + (size_t)(t0 + w * kR) * C + c;
+    T* out = static_cast<T*>(a.h) + (size_t)(t0 + w * R) * C + c;
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        if (kBounds && t0 + w * kR + r >= a.total) return;
-        const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+    for (int r = 0; r < R; ++r) {
+        if (kBounds && t0 + w * R + r >= a.total) return;
+        const int first = kBounds ? s_bounds.first_of[w * R + r] : -1;
         float xv[VEC];
         xr[r].get(xv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
             h[j] = kBounds && first >= 0 ? al[r][j] : fmaf(al[r][j], h[j], xv[j]);
         if (a.h) put(out + r * C, h);
-        const int last = kBounds ? s_bounds.last_of[w * kR + r] : -1;
+        const int last = kBounds ? s_bounds.last_of[w * R + r] : -1;
         if (kBounds && last >= 0 && a.final_state) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) a.final_state[(size_t)last * C + c + j] = h[j];
@@ -426,51 +435,51 @@ __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Ma
     }
 }
 
-template <int VEC, typename T>
+template <int VEC, int R, typename T>
 __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs a) {
     constexpr int CT = 32 * VEC;  // channels of a tile
     __shared__ __align__(16) Maps<VEC> s_maps;
-    __shared__ Bounds s_bounds;
+    __shared__ Bounds<8 * R> s_bounds;
     const int task = next_tile(a), tile = task / a.ctiles, c0 = (task % a.ctiles) * CT;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = tile * kRows + w * kR, mine = c0 + lane * VEC < a.C;
+    const int t = (tile * 8 + w) * R, mine = c0 + lane * VEC < a.C;
     const int c = mine ? c0 + lane * VEC : a.C - VEC;
-    Raw<VEC, T> xr[kR];
-    Raw<VEC, float> gr[kR];
+    Raw<VEC, T> xr[R];
+    Raw<VEC, float> gr[R];
     load_rows(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C, a.total - t);
     load_rows(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
-    find_bounds(a, tile * kRows, s_bounds);
+    find_bounds(a, tile * 8 * R, s_bounds);
     if (tile == 0) {
         if (c0 == 0) report_status(a);
         pass_empty(a, a.h0, a.final_state, c0, min(CT, a.C - c0));
     }
     if (s_bounds.plain)
-        fwd_tile<VEC, T, false>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+        fwd_tile<VEC, R, T, false>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
     else
-        fwd_tile<VEC, T, true>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+        fwd_tile<VEC, R, T, true>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
 }
 
-template <int VEC, typename T, bool kBounds>
+template <int VEC, int R, typename T, bool kBounds>
 __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Maps<VEC>& s_maps,
-                                         Maps<VEC>& s_back, const Bounds& s_bounds,
-                                         const Raw<VEC, T> (&xr)[kR], const Raw<VEC, T> (&dr)[kR],
-                                         const Raw<VEC, float> (&gr)[kR], int c, bool mine) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = tile * kRows;
+                                         Maps<VEC>& s_back, const Bounds<8 * R>& s_bounds,
+                                         const Raw<VEC, T> (&xr)[R], const Raw<VEC, T> (&dr)[R],
+                                         const Raw<VEC, float> (&gr)[R], int c, bool mine) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = tile * 8 * R;
     const size_t C = a.C;
     // the two maps of this warp's rows: of h, and of e from the right
-    float al[kR][VEC];
+    float al[R][VEC];
     {
         float G[VEC], Ge[VEC], b[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
+        for (int r = 0; r < R; ++r) {
             float gv[VEC], xv[VEC];
             gr[r].get(gv);
             xr[r].get(xv);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) al[r][j] = gate(gv[j], G[j]);
-            const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+            const int first = kBounds ? s_bounds.first_of[w * R + r] : -1;
             if (kBounds && first >= 0) state_of<VEC>(a.h0, first, C, c, b);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[r][j], b[j], xv[j]);
@@ -478,9 +487,9 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
         bool starts = false, ends = false;
         if (kBounds) {
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                starts |= s_bounds.first_of[w * kR + r] >= 0;
-                ends |= s_bounds.last_of[w * kR + r] >= 0;
+            for (int r = 0; r < R; ++r) {
+                starts |= s_bounds.first_of[w * R + r] >= 0;
+                ends |= s_bounds.last_of[w * R + r] >= 0;
             }
         }
 #pragma unroll
@@ -492,8 +501,8 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
 #pragma unroll
         for (int j = 0; j < VEC; ++j) b[j] = 0.f;
 #pragma unroll
-        for (int r = kR - 1; r >= 0; --r) {
-            const int last = kBounds ? s_bounds.last_of[w * kR + r] : -1;
+        for (int r = R - 1; r >= 0; --r) {
+            const int last = kBounds ? s_bounds.last_of[w * R + r] : -1;
             if (kBounds && last >= 0) state_of<VEC>(a.dfinal, last, C, c, b);
             float dv[VEC];
             dr[r].get(dv);
@@ -512,7 +521,7 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
             const float Gt = s_back.sum(ch), bt = s_back.template walk<true, false>(ch, 0.f);
             const bool known = tile == a.tiles - 1 || Gt == -INFINITY;
             if (tile > 0) publish(out, Gt, bt, known);
-            if (tile < a.tiles - 1 && !(kBounds && s_bounds.last_of[kRows - 1] >= 0)) {
+            if (tile < a.tiles - 1 && !(kBounds && s_bounds.last_of[8 * R - 1] >= 0)) {
                 e = look_back(a.words + c0 + ch, C, tile + 1, 1, a.tiles - 1 - tile, a.status);
                 if (!known && tile > 0)
                     publish(out, 0.f, applied(half_gate(Gt), bt, e), true);
@@ -522,20 +531,20 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
     } else if (threadIdx.x >= kThreads - 32 * VEC && c0 + threadIdx.x - (kThreads - 32 * VEC) < a.C) {
         // meanwhile (other warps): the states that enter the warps
         const int ch = threadIdx.x - (kThreads - 32 * VEC);
-        s_maps.template walk<false, true>(ch, a.entry[(size_t)tile * C + c0 + ch]);
+        s_maps.template walk<false, true>(ch, a.entry[(size_t)(t0 / kScanRows) * C + c0 + ch]);
     }
     __syncthreads();
 
     if (!mine) return;
-    float hb[kR][VEC], h[VEC], e[VEC];  // hb: the state before each row
+    float hb[R][VEC], h[VEC], e[VEC];  // hb: the state before each row
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         h[j] = s_maps.b[w][lane * VEC + j];
         e[j] = s_back.b[w][lane * VEC + j];
     }
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+    for (int r = 0; r < R; ++r) {
+        const int first = kBounds ? s_bounds.first_of[w * R + r] : -1;
         if (kBounds && first >= 0) state_of<VEC>(a.h0, first, C, c, h);
         float xv[VEC];
         xr[r].get(xv);
@@ -545,12 +554,12 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
             h[j] = fmaf(al[r][j], h[j], xv[j]);
         }
     }
-    T* dx = static_cast<T*>(a.dx) + (size_t)(t0 + w * kR) * C + c;
-    float* dg = a.dg + (size_t)(t0 + w * kR) * C + c;
+    T* dx = static_cast<T*>(a.dx) + (size_t)(t0 + w * R) * C + c;
+    float* dg = a.dg + (size_t)(t0 + w * R) * C + c;
 #pragma unroll
-    for (int r = kR - 1; r >= 0; --r) {
-        if (kBounds && t0 + w * kR + r >= a.total) continue;
-        const int last = kBounds ? s_bounds.last_of[w * kR + r] : -1;
+    for (int r = R - 1; r >= 0; --r) {
+        if (kBounds && t0 + w * R + r >= a.total) continue;
+        const int last = kBounds ? s_bounds.last_of[w * R + r] : -1;
         if (kBounds && last >= 0) state_of<VEC>(a.dfinal, last, C, c, e);
         float dv[VEC], dgv[VEC];
         dr[r].get(dv);
@@ -562,7 +571,7 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
         }
         put(dx + r * C, dv);
         put(dg + r * C, dgv);
-        const int first = kBounds ? s_bounds.first_of[w * kR + r] : -1;
+        const int first = kBounds ? s_bounds.first_of[w * R + r] : -1;
         if (kBounds && first >= 0 && a.dh0) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) a.dh0[(size_t)first * C + c + j] = e[j];
@@ -570,30 +579,30 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
     }
 }
 
-template <int VEC, typename T>
+template <int VEC, int R, typename T>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a) {
     constexpr int CT = 32 * VEC;
     __shared__ __align__(16) Maps<VEC> s_maps, s_back;
-    __shared__ Bounds s_bounds;
+    __shared__ Bounds<8 * R> s_bounds;
     const int task = next_tile(a), tile = a.tiles - 1 - task / a.ctiles;
     const int c0 = (task % a.ctiles) * CT;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = tile * kRows + w * kR, mine = c0 + lane * VEC < a.C;
+    const int t = (tile * 8 + w) * R, mine = c0 + lane * VEC < a.C;
     const int c = mine ? c0 + lane * VEC : a.C - VEC;
-    Raw<VEC, T> xr[kR], dr[kR];
-    Raw<VEC, float> gr[kR];
+    Raw<VEC, T> xr[R], dr[R];
+    Raw<VEC, float> gr[R];
     load_rows(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
     load_rows(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C, a.total - t);
     load_rows(dr, static_cast<const T*>(a.dout) + (size_t)t * a.C + c, a.C, a.total - t);
-    find_bounds(a, tile * kRows, s_bounds);
+    find_bounds(a, tile * 8 * R, s_bounds);
     if (tile == a.tiles - 1) {
         if (c0 == 0) report_status(a);
         pass_empty(a, a.dfinal, a.dh0, c0, min(CT, a.C - c0));
     }
     if (s_bounds.plain)
-        bwd_tile<VEC, T, false>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
+        bwd_tile<VEC, R, T, false>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
     else
-        bwd_tile<VEC, T, true>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
+        bwd_tile<VEC, R, T, true>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
 }
 
 // One token per sequence: state = exp(g) state + x, h = the state in T.
@@ -627,7 +636,7 @@ struct ScanSpace {
     uint32_t* ticket;
     uint64_t* words;
     float* entry;
-    size_t sync_bytes, total_bytes;
+    size_t total_bytes;
 };
 ScanSpace carve_scan(void* base, int total, int C, bool with_entry) {
     ScanSpace s{};
@@ -638,8 +647,7 @@ ScanSpace carve_scan(void* base, int total, int C, bool with_entry) {
     if (tiles > 1) {
         s.ticket = reinterpret_cast<uint32_t*>(p + off);
         s.words = reinterpret_cast<uint64_t*>(p + off + kAlign);
-        s.sync_bytes = kAlign + sizeof(uint64_t) * tiles * C;
-        off = align_up(off + s.sync_bytes);
+        off = align_up(off + kAlign + sizeof(uint64_t) * tiles * C);
     }
     if (with_entry) {
         s.entry = reinterpret_cast<float*>(p + off);
@@ -649,35 +657,41 @@ ScanSpace carve_scan(void* base, int total, int C, bool with_entry) {
     return s;
 }
 
-template <int VEC, typename T>
+template <int VEC, int R, typename T>
 cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t st) {
+    static_assert(8 * R % kScanRows == 0, "a tile begins at an entry state");
     a.status = s.status;
-    a.ticket = s.ticket;
-    a.words = s.words;
-    a.tiles = static_cast<int>(scan_tiles(a.total));
+    a.tiles = a.total > 0 ? static_cast<int>(((long long)a.total + 8 * R - 1) / (8 * R)) : 1;
     a.ctiles = (a.C + 32 * VEC - 1) / (32 * VEC);
     const long long grid = (long long)a.tiles * a.ctiles;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (s.ticket) {
-        const cudaError_t e = cudaMemsetAsync(s.ticket, 0xFF, s.sync_bytes, st);
+    if (a.tiles > 1) {
+        a.ticket = s.ticket;
+        a.words = s.words;
+        const cudaError_t e =
+            cudaMemsetAsync(s.ticket, 0xFF, kAlign + sizeof(uint64_t) * (size_t)a.tiles * a.C, st);
         if (e != cudaSuccess) return e;
     }
     if (backward)
-        scan_bwd_kernel<VEC, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+        scan_bwd_kernel<VEC, R, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
     else
-        scan_fwd_kernel<VEC, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+        scan_fwd_kernel<VEC, R, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, cudaStream_t st) {
+    // rows of C channels start on a 16-byte (fp32) or 8-byte (bf16) boundary
+    // when C is a multiple of 4; other sizes take one channel per lane, and
+    // four times the rows
+    if (a.C % 4 != 0) return run_scan<1, 32, T>(a, s, backward, st);
+    return run_scan<4, 8, T>(a, s, backward, st);
 }
 
 cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, kda_dtype_t dt,
                           cudaStream_t st) {
-    // rows of C channels start on a 16-byte (fp32) or 8-byte (bf16) boundary
-    // when C is a multiple of 4; other sizes take one channel per lane
-    if (dt == KDA_DTYPE_BF16)
-        return a.C % 4 == 0 ? run_scan<4, __nv_bfloat16>(a, s, backward, st)
-                            : run_scan<1, __nv_bfloat16>(a, s, backward, st);
-    return a.C % 4 == 0 ? run_scan<4, float>(a, s, backward, st)
-                        : run_scan<1, float>(a, s, backward, st);
+    return dt == KDA_DTYPE_BF16 ? dispatch_scan<__nv_bfloat16>(a, s, backward, st)
+                                : dispatch_scan<float>(a, s, backward, st);
 }
 
 }  // namespace
