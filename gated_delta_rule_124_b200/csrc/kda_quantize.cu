@@ -9,8 +9,9 @@
 // over those lanes, and over the CTA for a 128 x 128 block.  For the transpose
 // the tile goes to shared memory by asynchronous copies, and a thread takes two
 // neighbouring columns of 32 rows from there, so that it reads whole words
-// without bank conflicts and writes whole 32-byte sectors of two rows of the
-// result.
+// without bank conflicts, once for the maximum and once more for the codes (so
+// that six CTAs fit on an SM instead of three); the codes go through shared
+// memory too, so that eight lanes write 128 bytes of a row of the result.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
 
 // x [rows, cols] -> y8 [cols, pitch], pitch >= rows; blocks along x's rows.
 template <typename T, bool kRowBlocks, bool kVec>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 3)
     quantize_t_kernel(const T* __restrict__ x, int rows, int cols, int pitch,
                       uint8_t* __restrict__ y8, float* __restrict__ scale) {
     extern __shared__ __align__(16) uint8_t q_smem[];
@@ -179,13 +180,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     // two columns of 32 rows
     const int pair = threadIdx.x & 63, rg = threadIdx.x >> 6;
     const int c = cb * 128 + 2 * pair;
-    Two<T> v[32];
+    const T* mine = tile + rg * 32 * 128 + 2 * pair;
     float2 m = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < 32; ++r) {
-        v[r] = *reinterpret_cast<const Two<T>*>(tile + (rg * 32 + r) * 128 + 2 * pair);
-        max_abs(m, v[r]);
-    }
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) max_abs(m, *reinterpret_cast<const Two<T>*>(mine + r * 128));
     float f0, f1;
     if (kRowBlocks) {
         s_col[rg][2 * pair] = m.x;
@@ -207,21 +205,35 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
         if (threadIdx.x == 0) scale[(size_t)kb * CB + cb] = fp8_scale(all);
         f0 = f1 = fp8_factor(all);
     }
-    const int r0 = kb * 128 + rg * 32;
+    uint4 q[2][2];  // [column][half of the 32 rows]
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        if (r0 + 16 * half >= pitch) continue;
         uint32_t q0[4], q1[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const Two<T>* w = v + 16 * half + 4 * k;
+            Two<T> w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = *reinterpret_cast<const Two<T>*>(mine + (16 * half + 4 * k + j) * 128);
             q0[k] = fp8x4(w[0].lo() * f0, w[1].lo() * f0, w[2].lo() * f0, w[3].lo() * f0);
             q1[k] = fp8x4(w[0].hi() * f1, w[1].hi() * f1, w[2].hi() * f1, w[3].hi() * f1);
         }
-        uint8_t* out = y8 + (size_t)c * pitch + r0 + 16 * half;
-        if (c < cols) *reinterpret_cast<uint4*>(out) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
-        if (c + 1 < cols)
-            *reinterpret_cast<uint4*>(out + pitch) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+        q[0][half] = make_uint4(q0[0], q0[1], q0[2], q0[3]);
+        q[1][half] = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    }
+    __syncthreads();  // x has been read: the codes take its place, [column][144 bytes]
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+            *reinterpret_cast<uint4*>(q_smem + (2 * pair + e) * 144 + rg * 32 + half * 16) = q[e][half];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // eight lanes a row of the result
+        const int e = threadIdx.x + i * kThreads, row = e >> 3, piece = e & 7;
+        if (cb * 128 + row < cols && kb * 128 + piece * 16 < pitch)
+            *reinterpret_cast<uint4*>(y8 + (size_t)(cb * 128 + row) * pitch + kb * 128 + piece * 16) =
+                *reinterpret_cast<const uint4*>(q_smem + row * 144 + piece * 16);
     }
 }
 
