@@ -56,7 +56,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // NaN patterns no sum of logarithms has
 constexpr uint32_t kExit = 0xFFFFFFFEu;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kWindow = 4;             // published words a look-back requests at once
+constexpr int kWindow = 2;             // published words a look-back requests at once
 
 struct ScanArgs {
     const void* x;
