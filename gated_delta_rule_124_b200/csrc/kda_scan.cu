@@ -8,18 +8,21 @@
 // 8 bytes), so the kernels are bound by HBM: each element is read once and
 // written once, and the state crosses tiles through a few bytes per channel.
 //
-// Forward: the packed tokens are cut into tiles of kRows = 64 (regardless of
-// sequence bounds) by 128 channels.  A 256-thread CTA holds one tile in
-// registers: lane l of warp w holds channels [4 l, 4 l + 4) of rows [8 w, 8 w + 8),
-// all loads issued at once.  Each warp composes its eight rows, the CTA's
-// eight maps are composed through shared memory, and the tile's entry state
-// comes from a look-back over the tiles before it: each tile publishes its
-// composed map as soon as it has it and its exit state as soon as it knows its
-// entry state, so a tile composes its predecessors' maps until it meets an
-// exit state.  Then every warp runs the recurrence once more from its own
-// entry state, in the order of the definition, and writes h.  The first token
-// of a sequence replaces the state by the initial one, so a tile that holds
-// one knows its exit state without looking back.
+// Forward: the packed tokens are cut into tiles of 64 (256 where lanes have one
+// channel; regardless of sequence bounds) by 128 channels.  A 256-thread CTA holds
+// one tile in registers: lane l of warp w holds channels [4 l, 4 l + 4) of rows
+// [8 w, 8 w + 8), all loads issued at once.  Each warp composes its eight rows,
+// the CTA's eight maps are composed through shared memory, and the tile's entry
+// state comes from the tiles before it: each publishes its composed map, the last
+// one of a group also that of the group, and, once it knows it, the group's exit
+// state (a group is one tile, or several where there are few channels).  A tile's entry state is the exit state of the group before its own,
+// passed through the maps of its own group's tiles in their order; the exit state
+// of a group comes in the same way through the maps of groups.  So the state is
+// computed by one formula whatever was published first, and results do not
+// depend on the order of execution.  Then every warp runs the recurrence once
+// more from its own entry state, in the order of the definition, and writes h.
+// The first token of a sequence replaces the state by the initial one: a map that
+// forgets the state before it is an exit state by itself.
 //
 // A published value is one 64-bit word per (tile, channel), written and read
 // with single relaxed accesses, so that no fence is needed: {log2 of the gate
@@ -56,7 +59,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // NaN patterns no sum of logarithms has
 constexpr uint32_t kExit = 0xFFFFFFFEu;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kWindow = 2;             // published words a look-back requests at once
+constexpr int kDepth = 64;             // groups' maps a look-back passes at most
 
 struct ScanArgs {
     const void* x;
@@ -74,7 +77,7 @@ struct ScanArgs {
     float* dh0;             // [N, C] or NULL
     uint32_t* status;
     uint32_t* ticket;       // starts at 0xFFFFFFFF; NULL: one tile per channel block
-    uint64_t* words;        // [tiles, C]
+    uint64_t* words;        // [tiles, C] maps, then [groups, C]
     int tiles, ctiles;      // of the launched kernel's size
 };
 
@@ -162,36 +165,99 @@ __device__ __forceinline__ uint64_t read_word(const uint64_t* w) {
     return v;
 }
 
-// The state that enters a tile: composes the maps of the tiles before it (word
-// `first`, then `first + step`, ..., `count` of them) until one has published
-// its exit state; the last of them always does.
-__device__ float look_back(const uint64_t* words, size_t C, int first, int step, int count,
-                           uint32_t* status) {
-    float G = 0.f, h = 0.f;
-    for (int i = 0; i < count; i += kWindow) {
-        uint64_t v[kWindow];
-#pragma unroll
-        for (int j = 0; j < kWindow; ++j)
-            v[j] = read_word(words + (size_t)(first + step * min(i + j, count - 1)) * C);
-#pragma unroll
-        for (int j = 0; j < kWindow; ++j) {
-            if (i + j >= count) return h;
-            if (static_cast<uint32_t>(v[j]) == kNotYet) {
-                const uint64_t t0 = sm100::global_timer_ns();
-                do {
-                    v[j] = read_word(words + (size_t)(first + step * (i + j)) * C);
-                    if (sm100::global_timer_ns() - t0 > kWaitNs) {
-                        atomicOr(status, STATUS_TIMEOUT);
-                        return h;
-                    }
-                } while (static_cast<uint32_t>(v[j]) == kNotYet);
-            }
-            const uint32_t lo = static_cast<uint32_t>(v[j]);
-            const float b = __uint_as_float(static_cast<uint32_t>(v[j] >> 32));
-            h += scaled(b, ex2(0.5f * G));
-            if (lo == kExit) return h;
-            G += __uint_as_float(lo);
+// A word once it is there (for `exit_only`: once it is an exit state).
+__device__ __forceinline__ uint64_t await_word(const uint64_t* w, uint64_t v, bool exit_only,
+                                               uint32_t* status) {
+    const auto ready = [&] {
+        const uint32_t lo = static_cast<uint32_t>(v);
+        return exit_only ? lo == kExit : lo != kNotYet;
+    };
+    if (ready()) return v;
+    const uint64_t t0 = sm100::global_timer_ns();
+    do {
+        v = read_word(w);
+        if (ready()) return v;
+    } while (sm100::global_timer_ns() - t0 <= kWaitNs);
+    atomicOr(status, STATUS_TIMEOUT);
+    return kExit;  // (a state of 0; the outputs of the call are unspecified)
+}
+__device__ __forceinline__ float map_G(uint64_t v) {
+    return __uint_as_float(static_cast<uint32_t>(v));
+}
+__device__ __forceinline__ float map_b(uint64_t v) {
+    return __uint_as_float(static_cast<uint32_t>(v >> 32));
+}
+
+// The exit state of group g: from the nearest group before or at it that has
+// published its own (group 0 always does), through the maps of the groups between
+// in their order.  Maps found on the way back are kept (in local memory); behind
+// kDepth of them only an exit state will do.
+__device__ float group_exit(const uint64_t* groups, size_t C, int g, uint32_t* status) {
+    uint64_t kept[kDepth];
+    int n = 0;
+    const uint64_t* at = groups + (size_t)g * C;
+    uint64_t next = read_word(at);
+    float h = 0.f;
+    for (; g >= 0; --g, at -= C) {
+        uint64_t v = next;
+        if (g > 0) next = read_word(at - C);
+        v = await_word(at, v, n == kDepth || g == 0, status);
+        if (static_cast<uint32_t>(v) == kExit) {
+            h = map_b(v);
+            break;
         }
+        kept[n++] = v;
+    }
+    while (n > 0) {
+        const uint64_t v = kept[--n];
+        h = applied(half_gate(map_G(v)), map_b(v), h);
+    }
+    return h;
+}
+
+// Publishes a channel's map (G, b) of the tile at position pos (0: no tile is
+// before it), and its group's where it closes one; returns the state that enters
+// the tile (0 unless `needed`).
+template <int kTiles>
+__device__ float pass_tile(const ScanArgs& a, int ch, int pos, float G, float b, bool needed) {
+    const size_t C = a.C;
+    uint64_t* words = a.words + ch;
+    uint64_t* groups = kTiles == 1 ? words : words + (size_t)a.tiles * C;
+    const int in = pos % kTiles, g = pos / kTiles;
+    uint64_t* own = words + (size_t)(pos - in) * C;  // the group's first tile
+    const bool last = pos == a.tiles - 1, closes = in == kTiles - 1 && !last;
+    if (!last && !closes) publish(words + (size_t)pos * C, G, b, false);
+    // the maps of the group's tiles before this one, requested together
+    uint64_t v[kTiles > 1 ? kTiles - 1 : 1];
+    const bool all = needed || (closes && G != -INFINITY);
+#pragma unroll
+    for (int k = 0; k < kTiles - 1; ++k)
+        if (all && k < in) v[k] = read_word(own + (size_t)k * C);
+    float Gg = 0.f, bg = 0.f;
+    bool known = true;
+    if (closes) {
+        if (G != -INFINITY) {  // (a map that forgets needs none of the others)
+#pragma unroll
+            for (int k = 0; k < kTiles - 1; ++k) {
+                v[k] = await_word(own + (size_t)k * C, v[k], false, a.status);
+                bg = applied(half_gate(map_G(v[k])), map_b(v[k]), bg);
+                Gg += map_G(v[k]);
+            }
+        }
+        bg = applied(half_gate(G), b, bg);
+        Gg += G;
+        known = g == 0 || Gg == -INFINITY;
+        publish(groups + (size_t)g * C, Gg, bg, known);
+    }
+    float h = 0.f;
+    if (g > 0 && (needed || !known)) h = group_exit(groups, C, g - 1, a.status);
+    if (!known) publish(groups + (size_t)g * C, 0.f, applied(half_gate(Gg), bg, h), true);
+    if (!needed) return 0.f;
+#pragma unroll
+    for (int k = 0; k < kTiles - 1; ++k) {
+        if (k >= in) break;
+        if (!closes) v[k] = await_word(own + (size_t)k * C, v[k], false, a.status);
+        h = applied(half_gate(map_G(v[k])), map_b(v[k]), h);
     }
     return h;
 }
@@ -339,8 +405,15 @@ struct Maps {
     }
 };
 
+// Tiles of a group.  Where few channels leave many tiles of one sequence on the
+// device at once, groups keep the look-back short (262144 x 128: 94 us, 244
+// without); else the maps and exit states of single tiles do (65536 x 4096: 420
+// us, 448 with groups).
+constexpr int kGroup = 6;
+inline int group_of(int ctiles) { return ctiles < 8 ? kGroup : 1; }
+
 // kBounds: sequences begin or end in the tile, or the tokens do.
-template <int VEC, int R, typename T, bool kBounds>
+template <int VEC, int R, int GROUP, typename T, bool kBounds>
 __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Maps<VEC>& s_maps,
                                          const Bounds<8 * R>& s_bounds, const Raw<VEC, T> (&xr)[R],
                                          const Raw<VEC, float> (&gr)[R], int c, bool mine) {
@@ -383,20 +456,11 @@ __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Ma
     // warp's entry state
     if (threadIdx.x < 32 * VEC && c0 + threadIdx.x < a.C) {
         const int ch = threadIdx.x;
-        const bool last_tile = tile == a.tiles - 1;
         float h = 0.f;
-        if (a.ticket) {
-            uint64_t* out = a.words + (size_t)tile * C + c0 + ch;
-            const float Gt = s_maps.sum(ch), bt = s_maps.template walk<false, false>(ch, 0.f);
-            const bool known = tile == 0 || Gt == -INFINITY;
-            if (!last_tile) publish(out, Gt, bt, known);
-            // the entry state is used unless a sequence starts with the tile
-            if (tile > 0 && !(kBounds && s_bounds.first_of[0] >= 0)) {
-                h = look_back(a.words + c0 + ch, C, tile - 1, -1, tile, a.status);
-                if (!known && !last_tile)
-                    publish(out, 0.f, applied(half_gate(Gt), bt, h), true);
-            }
-        }
+        // (the entry state is used unless a sequence starts with the tile)
+        if (a.ticket)
+            h = pass_tile<GROUP>(a, c0 + ch, tile, s_maps.sum(ch), s_maps.template walk<false, false>(ch, 0.f),
+                          !(kBounds && s_bounds.first_of[0] >= 0));
         s_maps.template walk<false, true>(ch, h);
         if (a.entry) {  // the states before rows 0, kScanRows, ... of the tile
             constexpr int W = kScanRows / R < 1 ? 1 : kScanRows / R;
@@ -435,7 +499,7 @@ __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Ma
     }
 }
 
-template <int VEC, int R, typename T>
+template <int VEC, int R, int GROUP, typename T>
 __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs a) {
     constexpr int CT = 32 * VEC;  // channels of a tile
     __shared__ __align__(16) Maps<VEC> s_maps;
@@ -454,12 +518,12 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs a)
         pass_empty(a, a.h0, a.final_state, c0, min(CT, a.C - c0));
     }
     if (s_bounds.plain)
-        fwd_tile<VEC, R, T, false>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+        fwd_tile<VEC, R, GROUP, T, false>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
     else
-        fwd_tile<VEC, R, T, true>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+        fwd_tile<VEC, R, GROUP, T, true>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
 }
 
-template <int VEC, int R, typename T, bool kBounds>
+template <int VEC, int R, int GROUP, typename T, bool kBounds>
 __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Maps<VEC>& s_maps,
                                          Maps<VEC>& s_back, const Bounds<8 * R>& s_bounds,
                                          const Raw<VEC, T> (&xr)[R], const Raw<VEC, T> (&dr)[R],
@@ -516,17 +580,10 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
     if (threadIdx.x < 32 * VEC && c0 + threadIdx.x < a.C) {
         const int ch = threadIdx.x;
         float e = 0.f;
-        if (a.ticket) {
-            uint64_t* out = a.words + (size_t)tile * C + c0 + ch;
-            const float Gt = s_back.sum(ch), bt = s_back.template walk<true, false>(ch, 0.f);
-            const bool known = tile == a.tiles - 1 || Gt == -INFINITY;
-            if (tile > 0) publish(out, Gt, bt, known);
-            if (tile < a.tiles - 1 && !(kBounds && s_bounds.last_of[8 * R - 1] >= 0)) {
-                e = look_back(a.words + c0 + ch, C, tile + 1, 1, a.tiles - 1 - tile, a.status);
-                if (!known && tile > 0)
-                    publish(out, 0.f, applied(half_gate(Gt), bt, e), true);
-            }
-        }
+        if (a.ticket)
+            e = pass_tile<GROUP>(a, c0 + ch, a.tiles - 1 - tile, s_back.sum(ch),
+                          s_back.template walk<true, false>(ch, 0.f),
+                          !(kBounds && s_bounds.last_of[8 * R - 1] >= 0));
         s_back.template walk<true, true>(ch, e);
     } else if (threadIdx.x >= kThreads - 32 * VEC && c0 + threadIdx.x - (kThreads - 32 * VEC) < a.C) {
         // meanwhile (other warps): the states that enter the warps
@@ -579,7 +636,7 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
     }
 }
 
-template <int VEC, int R, typename T>
+template <int VEC, int R, int GROUP, typename T>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a) {
     constexpr int CT = 32 * VEC;
     __shared__ __align__(16) Maps<VEC> s_maps, s_back;
@@ -600,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a)
         pass_empty(a, a.dfinal, a.dh0, c0, min(CT, a.C - c0));
     }
     if (s_bounds.plain)
-        bwd_tile<VEC, R, T, false>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
+        bwd_tile<VEC, R, GROUP, T, false>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
     else
-        bwd_tile<VEC, R, T, true>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
+        bwd_tile<VEC, R, GROUP, T, true>(a, tile, c0, s_maps, s_back, s_bounds, xr, dr, gr, c, mine);
 }
 
 // One token per sequence: state = exp(g) state + x, h = the state in T.
@@ -629,8 +686,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* __restrict__ x,
 }
 
 // The workspace of a scan: [0, 256) status word, then the ticket (256 bytes)
-// and one 64-bit word per (tile, channel) -- none of these two when the tokens
-// fit in one tile -- and, for a backward without entry states, those.
+// and one 64-bit word per (tile, channel) and per (group of tiles, channel) --
+// none of these when the tokens fit in one tile -- and, for a backward without entry states, those.
 struct ScanSpace {
     uint32_t* status;
     uint32_t* ticket;
@@ -647,7 +704,7 @@ ScanSpace carve_scan(void* base, int total, int C, bool with_entry) {
     if (tiles > 1) {
         s.ticket = reinterpret_cast<uint32_t*>(p + off);
         s.words = reinterpret_cast<uint64_t*>(p + off + kAlign);
-        off = align_up(off + kAlign + sizeof(uint64_t) * tiles * C);
+        off = align_up(off + kAlign + sizeof(uint64_t) * (tiles + tiles / kGroup) * C);
     }
     if (with_entry) {
         s.entry = reinterpret_cast<float*>(p + off);
@@ -668,14 +725,16 @@ cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t
     if (a.tiles > 1) {
         a.ticket = s.ticket;
         a.words = s.words;
+        const int words = group_of(a.ctiles) == 1 ? a.tiles : a.tiles + a.tiles / kGroup;
         const cudaError_t e =
-            cudaMemsetAsync(s.ticket, 0xFF, kAlign + sizeof(uint64_t) * (size_t)a.tiles * a.C, st);
+            cudaMemsetAsync(s.ticket, 0xFF, kAlign + sizeof(uint64_t) * a.C * (size_t)words, st);
         if (e != cudaSuccess) return e;
     }
-    if (backward)
-        scan_bwd_kernel<VEC, R, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
-    else
-        scan_fwd_kernel<VEC, R, T><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+    const bool one = group_of(a.ctiles) == 1;
+    const auto kernel =
+        backward ? (one ? scan_bwd_kernel<VEC, R, 1, T> : scan_bwd_kernel<VEC, R, kGroup, T>)
+                 : (one ? scan_fwd_kernel<VEC, R, 1, T> : scan_fwd_kernel<VEC, R, kGroup, T>);
+    kernel<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -514,9 +514,7 @@ kda_status_t kda_layer_decode_step(const void* xq, const void* xk, const void* x
  * An empty sequence passes its initial state on.  The state is fp32 throughout
  * and h one rounding of it; a NaN or an infinity stays inside its channel and
  * sequence.  One pass over x and g whatever the lengths: long sequences are
- * split over time, and results do not depend on the order of execution beyond
- * the rounding of states at the split (the tiles compose in one order, but
- * from the maps or from an exit state, whichever is there).
+ * split over time.  Results have the same bits in every run.
  * Workspace: kda_linear_scan_workspace_size(total, H, d) bytes, 256-byte
  *      aligned, starting with the status word of kda_get_device_status
  *      (KDA_ERR_BAD_SEQLENS, KDA_ERR_TIMEOUT: outputs unspecified).  Calls

@@ -226,6 +226,24 @@ def test_long_sequence_on_few_channels():
     assert torch.equal(final[0], h[-1])
 
 
+@pytest.mark.parametrize("T,H,d,dtype", [(30_000, 1, 128, "bf16"), (6_000, 16, 128, "bf16"),
+                                         (30_000, 1, 24, "f32"), (20_000, 1, 33, "bf16")])
+def test_results_have_the_same_bits_in_every_run(T, H, d, dtype):
+    """Few channels (tiles in groups), many, one channel per lane; more tiles than
+    fit on the device at once."""
+    lens = [T // 2 + 7, T - T // 2 - 7]
+    X, G, I, D, F = cuda(*make(14, lens, H, d, dtype, -3.0))
+    cu = offsets(lens)
+
+    def call():
+        h, final, entry = kda.linear_scan(X, G, I, cu_seqlens=cu, output_entry_states=True)
+        return (h, final, entry, *kda.linear_scan_bwd(X, G, D, I, F, cu_seqlens=cu,
+                                                      entry_states=entry))
+    first = call()
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(first, call()))
+
+
 def test_nan_and_infinity_stay_in_their_sequence_and_channel():
     lens = [100, 70, 90]
     x, g, init, _, _ = make(9, lens, 1, 8, "f32")
