@@ -237,27 +237,31 @@ __global__ void __launch_bounds__(RowGroup<TPR>::kThreads, RowGroup<TPR>::kBackw
     }
 }
 
-// dw[c] = sum over parts, 32 columns a CTA: 8 warps take every eighth part,
-// then one adds their sums.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ parts, int n,
-                                                        int D, float* __restrict__ dw) {
-    __shared__ float s_sum[8][32];
+// dw[c] = sum over parts, 32 columns a CTA: 32 warps take every 32nd part, all
+// loads of a warp in flight at once (the parts are in L2: bound by latency), then
+// one warp adds their sums.
+constexpr int kSumWarps = 32;
+constexpr int kPartsPerWarp = (kMaxParts + kSumWarps - 1) / kSumWarps;
+__global__ void __launch_bounds__(32 * kSumWarps) sum_parts_kernel(const float* __restrict__ parts,
+                                                                   int n, int D,
+                                                                   float* __restrict__ dw) {
+    __shared__ float s_sum[kSumWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (c < D) {
-        int i = w;
-        for (; i + 24 < n; i += 32) {
+    float v[kPartsPerWarp];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[u] += parts[(size_t)(i + 8 * u) * D + c];
-        }
-        for (; i < n; i += 8) acc[0] += parts[(size_t)i * D + c];
+    for (int u = 0; u < kPartsPerWarp; ++u) {
+        const int i = w + u * kSumWarps;
+        v[u] = i < n && c < D ? parts[(size_t)i * D + c] : 0.f;
     }
-    s_sum[w][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    float acc = 0.f;
+#pragma unroll
+    for (int u = 0; u < kPartsPerWarp; ++u) acc += v[u];
+    s_sum[w][lane] = acc;
     __syncthreads();
     if (w == 0 && c < D) {
         float x = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x += s_sum[i][lane];
+        for (int i = 0; i < kSumWarps; ++i) x += s_sum[i][lane];
         dw[c] = x;
     }
 }
@@ -299,7 +303,7 @@ cudaError_t norm_bwd_case(const void* s, const float* w, const void* dy, const v
         add_rms_norm_bwd_kernel<T, TPR, VPT><<<grid, G::kThreads, 0, st>>>(
             static_cast<const T*>(s), w, static_cast<const T*>(dy), static_cast<const T*>(dsum),
             rows, D, eps, static_cast<T*>(dx), parts);
-    sum_parts_kernel<<<(D + 31) / 32, 256, 0, st>>>(parts, static_cast<int>(grid) * G::kRowsPerCta,
+    sum_parts_kernel<<<(D + 31) / 32, 32 * kSumWarps, 0, st>>>(parts, static_cast<int>(grid) * G::kRowsPerCta,
                                                     D, dw);
     return cudaGetLastError();
 }
