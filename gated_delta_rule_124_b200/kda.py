@@ -885,11 +885,27 @@ def linear_scan_bwd(x, g, dout, initial_state=None, dfinal_state=None, cu_seqlen
     return dx, dg, dh0
 
 
+def _check_leaves(ctx, device):
+    """torch passes a leaf's gradient on on the stream that its accumulation node was
+    made on, and that node lives as long as any graph of the leaf does.  The legacy
+    default stream cannot join a capture: a backward pass captured while an eager
+    graph from that stream lives would end the process, so the forward refuses."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    capturing = torch.cuda.is_current_stream_capturing()
+    for node, _ in ctx.next_functions:
+        if node is not None and hasattr(node, "variable"):
+            if node.metadata.setdefault("kda_stream", stream) == 0 and capturing:
+                raise RuntimeError("capturing a differentiable call while an eager graph of the "
+                                   "same leaves, made on the default stream, is alive: release "
+                                   "it (its outputs or loss) first")
+
+
 class LinearScan(torch.autograd.Function):
     """Differentiable linear_scan; keeps its inputs and one state per 64 tokens."""
 
     @staticmethod
     def forward(ctx, x, g, initial_state, cu_seqlens):
+        _check_leaves(ctx, x.device)
         ctx.set_materialize_grads(False)
         h, hN, entry = linear_scan(x, g, initial_state, cu_seqlens=cu_seqlens,
                                    output_entry_states=True)
@@ -981,6 +997,7 @@ class AddRMSNorm(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w, residual, eps):
+        _check_leaves(ctx, x.device)
         ctx.set_materialize_grads(False)
         s, y = add_rms_norm(x, w, residual, eps=eps)
         ctx.eps, ctx.has_residual = eps, residual is not None
@@ -1050,6 +1067,7 @@ class Fp8Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w):
+        _check_leaves(ctx, x.device)
         x2 = x.reshape(-1, x.shape[-1]).contiguous()
         w8, w_scale = quantize_fp8(w, block_rows=128)
         x8, x_scale = quantize_fp8(x2)

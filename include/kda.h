@@ -517,8 +517,9 @@ kda_status_t kda_layer_decode_step(const void* xq, const void* xk, const void* x
  * split over time.  Results have the same bits in every run.
  * Workspace: kda_linear_scan_workspace_size(total, H, d) bytes, 256-byte
  *      aligned, starting with the status word of kda_get_device_status
- *      (KDA_ERR_BAD_SEQLENS, KDA_ERR_TIMEOUT: outputs unspecified).  Calls
- *      whose work may overlap need workspaces of their own.
+ *      (KDA_ERR_BAD_SEQLENS, KDA_ERR_TIMEOUT: outputs unspecified).  Calls,
+ *      and captured graphs, whose work may overlap need workspaces of their
+ *      own.
  * Shapes: H >= 1, d >= 1, H d <= 2^24 (multiples of 4 run four channels a lane).
  *
  * kda_linear_scan_bwd: gradients of sum(h * dout) + sum(final_state *
@@ -578,7 +579,8 @@ kda_status_t kda_linear_scan_step(const void* x, const float* g, const float* st
  * Out: sum [rows, D] (dtype) or NULL: s; y [rows, D] (dtype) or NULL; y8
  *      [rows, kda_fp8_pitch(D)] and y8_scale [ceil(D / 128), rows] fp32, both
  *      or neither; at least one of y and y8.  sum may be x or residual.
- * Shapes: D a multiple of 8, 8 <= D <= 16384.  rows = 0 does nothing.
+ * Shapes: D a multiple of 8, 8 <= D <= 16384.  rows = 0 does nothing.  Squares are
+ * summed in fp32: a row whose mean square is beyond its range gives zeros.
  *
  * kda_add_rms_norm_bwd: gradients of sum(y * dy) + sum(sum * dsum).
  * In:  s [rows, D]: sum as the forward wrote it (or x without a residual); w;

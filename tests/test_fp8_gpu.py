@@ -132,6 +132,18 @@ def test_norm_backward_matches_the_formula(rows, D, dtype):
         assert (np.abs(f64(dw) - rw) <= (rows / 4 + 80 + rel / U) * U * terms).all()
 
 
+def test_norm_backward_into_the_sums_gradient():
+    rows, D = 700, 520
+    s, dy = randn(60, rows, D, dtype="bf16").cuda(), randn(61, rows, D, dtype="bf16").cuda()
+    ds, w = randn(62, rows, D, dtype="bf16").cuda(), (1 + randn(63, D, scale=0.1)).cuda()
+    want_dx, want_dw = kda.add_rms_norm_bwd(s, w, dy, ds)
+    dw = torch.empty_like(w)
+    ws = torch.empty(kda.kda_add_rms_norm_bwd_workspace_size(rows, D), dtype=torch.uint8,
+                     device="cuda")
+    kda.kda_add_rms_norm_bwd(s, w, dy, ds, rows, D, "bf16", 1e-6, ds, dw, ws)
+    assert torch.equal(ds, want_dx) and torch.equal(dw, want_dw)
+
+
 def test_norm_backward_is_the_difference_quotient():
     rows, D, h = 3, 40, 1e-5
     s, dy, ds = f64(randn(10, rows, D)), f64(randn(11, rows, D)), f64(randn(12, rows, D))
@@ -304,6 +316,44 @@ def test_linear_and_its_gradients():
         tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -3 * 3 * np.abs(a).max(1, keepdims=True) * np.abs(b).max()
         assert (np.abs(f64(got) - want) <= tol).all()
         assert np.abs(f64(got) - want).mean() <= 2.0 ** -8 * np.abs(want).mean()
+
+
+def test_gradients_captured_into_a_graph():
+    """Forward and backward of the three differentiable calls in one graph, replayed
+    on new inputs; refused while an eager graph of the same leaves lives."""
+    T, D = 70, 256
+    x, r = (randn(70 + i, T, D, dtype="bf16").cuda().requires_grad_() for i in range(2))
+    w_norm = torch.ones(D, device="cuda", requires_grad=True)
+    w = randn(72, D, D, dtype="bf16", scale=D ** -0.5).cuda().requires_grad_()
+    g = -torch.rand(T, 2, D // 2, device="cuda")
+    dy = randn(73, T, D, dtype="bf16").cuda()
+
+    def step():
+        s, y = kda.residual_rms_norm(x, w_norm, r)
+        h, _ = kda.gated_linear_scan(kda.fp8_linear(y, w).view(T, 2, D // 2), g)
+        grads = torch.autograd.grad([h.reshape(T, D), s], [x, w_norm, r, w], [dy, dy])
+        return [t.detach() for t in (h, s, *grads)]
+    alive = kda.fp8_linear(x, w)
+    with pytest.raises(RuntimeError, match="eager graph"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            step()
+    del alive
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    with torch.no_grad():
+        x.copy_(randn(74, T, D, dtype="bf16"))
+        dy.copy_(randn(75, T, D, dtype="bf16"))
+    graph.replay()
+    want = step()
+    torch.cuda.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
 
 
 def test_a_layer_from_its_parts():

@@ -186,6 +186,8 @@ def test_batch_by_time_layout_without_states():
     dx, dg, dh0 = kda.linear_scan_bwd(X, G, D)
     check_backward(x, g, None, dout, None, [T] * B,
                    (dx.view(-1, H, d), dg.view(-1, H, d), dh0), "bf16")
+    empty = kda.linear_scan(X[:, :0], G[:, :0], init3 := torch.randn(B, H, d, device="cuda"))
+    assert empty[0].shape == (B, 0, H, d) and torch.equal(empty[1], init3)
     h2, none = kda.linear_scan(X, G, output_final_state=False)
     assert none is None and torch.equal(h, h2)
 
