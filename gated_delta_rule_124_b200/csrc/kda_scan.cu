@@ -15,12 +15,13 @@
 // the CTA's eight maps are composed through shared memory, and the tile's entry
 // state comes from the tiles before it: each publishes its composed map, the last
 // one of a group also that of the group, and, once it knows it, the group's exit
-// state (a group is one tile, or several where there are few channels).  A tile's entry state is the exit state of the group before its own,
-// passed through the maps of its own group's tiles in their order; the exit state
-// of a group comes in the same way through the maps of groups.  So the state is
-// computed by one formula whatever was published first, and results do not
-// depend on the order of execution.  Then every warp runs the recurrence once
-// more from its own entry state, in the order of the definition, and writes h.
+// state (a group is one tile, or several where there are few channels).  A tile's
+// entry state is the exit state of the group before its own, passed through the
+// maps of its own group's tiles in their order; the exit state of a group comes in
+// the same way through the maps of groups.  So the state is computed by one
+// formula whatever was published first, and results do not depend on the order
+// of execution.  Then every warp runs the recurrence once more from its own entry
+// state, in the order of the definition, and writes h.
 // The first token of a sequence replaces the state by the initial one: a map that
 // forgets the state before it is an exit state by itself.
 //
@@ -56,7 +57,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 // A warp has R rows of a tile and a lane VEC channels; a tile has 8 R rows, a
 // multiple of the kScanRows between entry states.
-constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // NaN patterns no sum of logarithms has
+constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // NaNs: no sum of logarithms is one
 constexpr uint32_t kExit = 0xFFFFFFFEu;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kDepth = 64;             // groups' maps a look-back passes at most
@@ -130,10 +131,13 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // exp(g), and its logarithm to base 2 added to G: 2^y (1 + r ln 2) with y + r =
 // g log2(e) in two floats, so that the error stays that of ex2 (2 units in the
-// last place) for every g.
+// last place).  g is held above -1e25 first (a NaN stays one): exp is 0 there all
+// the same, and y, r and G stay finite.  So g = -inf is a gate of 0, which any
+// state meets as in the definition, and G = -inf is left to the maps below.
 __device__ __forceinline__ float gate(float g, float& G) {
     constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299e-8f;  // log2(e)
     constexpr float kLn2 = 0.693147182464599609375f;
+    asm("max.NaN.f32 %0, %0, 0fE9045951;" : "+f"(g));
     const float y = g * kHi;
     const float r = fmaf(g, kHi, -y) + g * kLo;
     G += y;
@@ -155,7 +159,7 @@ __device__ __forceinline__ float applied(float e, float b, float h) {
 }
 
 __device__ __forceinline__ void publish(uint64_t* w, float G, float b, bool exit_state) {
-    const uint32_t lo = exit_state ? kExit : (G != G ? 0x7FFFFFFFu : __float_as_uint(G));
+    const uint32_t lo = exit_state ? kExit : __float_as_uint(G);
     const uint64_t v = static_cast<uint64_t>(__float_as_uint(b)) << 32 | lo;
     asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(w), "l"(v) : "memory");
 }
@@ -256,7 +260,7 @@ __device__ float pass_tile(const ScanArgs& a, int ch, int pos, float G, float b,
 #pragma unroll
     for (int k = 0; k < kTiles - 1; ++k) {
         if (k >= in) break;
-        if (!closes) v[k] = await_word(own + (size_t)k * C, v[k], false, a.status);
+        v[k] = await_word(own + (size_t)k * C, v[k], false, a.status);
         h = applied(half_gate(map_G(v[k])), map_b(v[k]), h);
     }
     return h;
@@ -379,8 +383,11 @@ struct Maps {
     __device__ void set(int w, int lane, const float (&g)[VEC], const float (&v)[VEC]) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            G[w][lane * VEC + j] = g[j];
-            e[w][lane * VEC + j] = half_gate(g[j]);
+            // (a NaN, or gates beyond fp32's range, are in v too; here they would
+            // turn the -inf of a later sequence's start into NaN)
+            const float sum = fminf(g[j], 1e30f);
+            G[w][lane * VEC + j] = sum;
+            e[w][lane * VEC + j] = half_gate(sum);
             b[w][lane * VEC + j] = v[j];
         }
     }

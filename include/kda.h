@@ -506,7 +506,9 @@ kda_status_t kda_layer_decode_step(const void* xq, const void* xk, const void* x
  * kda_linear_scan_fwd
  * In:  x [total, H, d] (dtype); g [total, H, d] fp32; initial_state [num_seqs,
  *      H, d] fp32 or NULL (zeros); cu_seqlens / B / T / num_seqs as for
- *      kda_chunk_fwd.  g is any finite value.
+ *      kda_chunk_fwd.  g is any value for which exp(g) is finite (one
+ *      beyond that gives states that are not); with -inf the gate is 0, and the
+ *      state starts again from x_t.
  * Out: h [total, H, d] (dtype), not aliasing the inputs; final_state [num_seqs,
  *      H, d] fp32 or NULL (not written), which may be initial_state;
  *      entry_states [kda_linear_scan_num_entries(total), H, d] fp32 or NULL:

@@ -260,6 +260,81 @@ def test_nan_and_infinity_stay_in_their_sequence_and_channel():
     assert torch.isfinite(final[2]).all()
 
 
+@pytest.mark.parametrize("bad_gate", [float("nan"), 3e38])
+@pytest.mark.parametrize("C", [8, 7, 128, 1100])
+def test_a_nan_gate_stays_in_its_sequence(C, bad_gate):
+    """Sequences that begin inside the tile, and the group of tiles, of the NaN."""
+    lens = [90, 20, 200, 1000, 700, 300, 1]
+    x, g, init, dout, dfin = make(15, lens, 1, C, "f32")
+    starts = np.cumsum([0] + lens)
+    for n in (0, 2, 4):
+        g[starts[n] + lens[n] // 2, 0, 1] = bad_gate
+    X, G, I, D, F = cuda(x, g, init, dout, dfin)
+    cu = offsets(lens)
+    h, final, entry = kda.linear_scan(X, G, I, cu_seqlens=cu, output_entry_states=True)
+    dx, dg, dh0 = kda.linear_scan_bwd(X, G, D, I, F, cu_seqlens=cu, entry_states=entry)
+    for n, at, length in seq_slices(lens):
+        mid, end = at + length // 2, at + length
+        for out, a, b in ((h, mid, end), (dx, at, mid), (dg, at, end)):
+            bad = torch.zeros(length, C, dtype=torch.bool)
+            if n in (0, 2, 4):
+                bad[a - at:b - at, 1] = True
+            got = ~torch.isfinite(out[at:end, 0].cpu())
+            assert torch.equal(got, bad), (n, torch.nonzero(got != bad)[:4])
+    bad = torch.zeros(len(lens), C, dtype=torch.bool)
+    bad[[0, 2, 4], 1] = True
+    assert torch.equal(~torch.isfinite(final[:, 0].cpu()), bad)
+    assert torch.equal(~torch.isfinite(dh0[:, 0].cpu()), bad)
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min, -1e9])
+@pytest.mark.parametrize("C", [8, 5, 1024])
+def test_gates_of_zero_start_the_state_again(C, low):
+    """As sequences of their own do: the same values, within the bounds."""
+    lens = [130, 64, 1, 500, 305]
+    total = sum(lens)
+    x, g, init, dout, _ = make(16, [total], 1, C, "f32")
+    for _, at, _ in list(seq_slices(lens))[1:]:
+        g[at] = low
+    X, G, I, D = cuda(x, g, init, dout)
+    h, final = kda.linear_scan(X, G, I)
+    check_forward(x, g, init, [total], h, final, "f32")
+    check_backward(x, g, init, dout, None, [total], kda.linear_scan_bwd(X, G, D, I), "f32")
+
+
+def test_gates_beyond_the_range_of_exp():
+    x, g = torch.ones(3, 1, 4), torch.tensor([0.0, 90.0, 3e38]).view(3, 1, 1).expand(3, 1, 4)
+    h, _ = kda.linear_scan(*cuda(x, g.contiguous(), torch.ones(1, 1, 4)))
+    assert (h[0] == 2).all() and not torch.isfinite(h[1:]).any()
+
+
+@pytest.mark.parametrize("C,every", [(8, 97), (128, 384), (128, 161), (33, 1531)])
+def test_many_sequences_on_few_channels(C, every):
+    """Starts in every place of a tile and of a group of tiles, far more tiles than
+    run at once."""
+    T = 120_000
+    lens = [every] * (T // every) + [T % every]
+    x, g, init, _, _ = make(17, lens, 1, C, "f32", -3.0)
+    X, G, I = cuda(x, g, init)
+    for _ in range(3):
+        h, final = kda.linear_scan(X, G, I, cu_seqlens=offsets(lens))
+    n = T // every * every      # the whole sequences, side by side
+    H64 = I[:-1].double()
+    a = G[:n].view(-1, every, 1, C).double().exp()
+    b = X[:n].view(-1, every, 1, C).double()
+    E, M = torch.zeros_like(H64), H64.abs()
+    at = torch.arange(0, n, every, device="cuda")
+    for t in range(every):
+        if t:
+            E = torch.where(((at + t) % TILE == 0).view(-1, 1, 1), E + 64 * U * M, E)
+        H64 = a[:, t] * H64 + b[:, t]
+        E = a[:, t] * (E + 6 * U * M)
+        M = a[:, t] * M + b[:, t].abs()
+        E = E + U * M
+        assert ((h[:n].view(-1, every, 1, C)[:, t].double() - H64).abs() <= E + TINY).all()
+    assert ((final[:-1].double() - H64).abs() <= E + TINY).all()
+
+
 def test_step_continues_a_prefill():
     N, H, d, T = 5, 3, 20, 70
     x, g, init, _, _ = make(10, [T] * N, H, d, "bf16")
