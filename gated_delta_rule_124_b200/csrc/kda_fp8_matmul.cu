@@ -68,7 +68,7 @@ struct MatmulArgs {
     const float* sb;  // [KB, N] or [KB, ceil(N / 128)]
     void* out;        // [M, N]
     int M, N, KB, NB; // NB: columns of sb
-    int out_bf16;
+    int out_bf16, out_wide;  // wide: out starts on 32 bytes
     int ntm, tiles, split;
 };
 
@@ -185,7 +185,12 @@ __device__ __forceinline__ float half_of(uint64_t v, int j) {
     return __uint_as_float(static_cast<uint32_t>(v >> (32 * j)));
 }
 
-__device__ __forceinline__ void store32(void* p, uint4 a, uint4 b) {
+__device__ __forceinline__ void store32(const MatmulArgs& args, void* p, uint4 a, uint4 b) {
+    if (!args.out_wide) {
+        static_cast<uint4*>(p)[0] = a;
+        static_cast<uint4*>(p)[1] = b;
+        return;
+    }
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
                  "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                  : "memory");
@@ -254,12 +259,12 @@ struct RowSums {
         const int left = a.N - n;  // columns of the output from n on
         if (a.out_bf16) {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + o;
-            if (a.N % 16 == 0) {  // rows, and 16 columns, start on 32 bytes
+            if (a.N % 16 == 0) {  // rows, and 16 columns, are whole 32-byte pieces
 #pragma unroll
                 for (int j = 0; j < NC / 16; ++j) {
                     if (16 * j >= left) break;
                     const uint64_t* v = acc + 8 * j;
-                    store32(out + 16 * j,
+                    store32(a, out + 16 * j,
                             make_uint4(bf16_pair(v[0]), bf16_pair(v[1]), bf16_pair(v[2]), bf16_pair(v[3])),
                             make_uint4(bf16_pair(v[4]), bf16_pair(v[5]), bf16_pair(v[6]), bf16_pair(v[7])));
                 }
@@ -275,7 +280,7 @@ struct RowSums {
                 for (int j = 0; j < NC / 8; ++j) {
                     if (8 * j >= left) break;
                     const uint64_t* v = acc + 4 * j;
-                    store32(out + 8 * j, words(v[0], v[1]), words(v[2], v[3]));
+                    store32(a, out + 8 * j, words(v[0], v[1]), words(v[2], v[3]));
                 }
             } else {
 #pragma unroll
@@ -696,6 +701,7 @@ cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale,
     a.KB = blocks128(K);
     a.NB = b_rows ? N : blocks128(N);
     a.out_bf16 = out_dt == KDA_DTYPE_BF16;
+    a.out_wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
     a.ntm = static_cast<int>(((long long)M + kRowsA - 1) / kRowsA);
     a.split = split;
     const long long tiles = (long long)a.ntm * (((long long)N + bn - 1) / bn);
