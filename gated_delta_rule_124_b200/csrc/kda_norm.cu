@@ -36,7 +36,7 @@ struct RowGroup {
     static constexpr int kThreads = TPR < 128 ? 128 : TPR;
     static constexpr int kRowsPerCta = kThreads / TPR;
     // CTAs of an SM (768 threads forward, 512 backward: the registers allow it)
-    static constexpr int kForward = TPR > 512 ? 1 : TPR == 512 ? 1 : 768 / kThreads;
+    static constexpr int kForward = 768 / kThreads;
     static constexpr int kBackward = 512 / kThreads;
 };
 
@@ -151,9 +151,10 @@ __global__ void __launch_bounds__(RowGroup<TPR>::kThreads, RowGroup<TPR>::kForwa
             if (y && live && c < D) store_vec8(y + row * D + c, v[i]);
             if (y8) {
                 const float amax = max16(max_abs8(v[i]));
+                // (behind D zeros, in a row of NaN too)
                 if (live && c < pitch)
                     *reinterpret_cast<uint2*>(y8 + row * pitch + c) =
-                        quantize8(v[i], fp8_factor(amax));
+                        c < D ? quantize8(v[i], fp8_factor(amax)) : make_uint2(0u, 0u);
                 if (live && c < D && (t & 15) == 0)
                     y8_scale[(size_t)(c / 128) * rows + row] = fp8_scale(amax);
             }
@@ -296,15 +297,15 @@ cudaError_t norm_bwd_case(const void* s, const float* w, const void* dy, const v
                           cudaStream_t st) {
     using G = RowGroup<TPR>;
     constexpr int most = kMaxParts / G::kRowsPerCta;
-    const int ctas = (rows + G::kRowsPerCta - 1) / G::kRowsPerCta;
+    const long long ctas = ((long long)rows + G::kRowsPerCta - 1) / G::kRowsPerCta;
     const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
     float* parts = static_cast<float*>(ws);
     if (grid > 0)
         add_rms_norm_bwd_kernel<T, TPR, VPT><<<grid, G::kThreads, 0, st>>>(
             static_cast<const T*>(s), w, static_cast<const T*>(dy), static_cast<const T*>(dsum),
             rows, D, eps, static_cast<T*>(dx), parts);
-    sum_parts_kernel<<<(D + 31) / 32, 32 * kSumWarps, 0, st>>>(parts, static_cast<int>(grid) * G::kRowsPerCta,
-                                                    D, dw);
+    sum_parts_kernel<<<(D + 31) / 32, 32 * kSumWarps, 0, st>>>(
+        parts, static_cast<int>(grid) * G::kRowsPerCta, D, dw);
     return cudaGetLastError();
 }
 
