@@ -19,6 +19,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
@@ -217,6 +218,8 @@ def _args(what, *pairs):
         elif d != device:
             raise ValueError(f"{what}: tensors on different devices ({device} and {d})")
         out.append(t.data_ptr())
+    if device is not None and device < 0:
+        raise ValueError(f"{what}: the tensors are not on a GPU")
     return out, device
 
 
@@ -231,7 +234,7 @@ def _enqueue(name, device, stream, check, *args) -> int:
     current stream of the tensors' device, which is the current device during the
     call."""
     fn = getattr(_lib or load(), name)
-    if device is None or device < 0:   # raw addresses, or nothing on a GPU
+    if device is None:   # raw addresses
         return _ret(fn(*args, _stream(stream)), name, check)
     if stream is None:
         stream = _current_stream(device)
@@ -913,6 +916,7 @@ class LinearScan(torch.autograd.Function):
         return h, hN
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, dhN):
         x, g, h0, cu, entry = ctx.saved_tensors
         dh = torch.zeros_like(x) if dh is None else dh.to(x.dtype).contiguous()
@@ -970,8 +974,8 @@ def add_rms_norm(x, w, residual=None, eps=1e-6, quantize=False, sum=None, stream
         scale = torch.empty(_blocks128(D), rows, dtype=torch.float32, device=x.device)
     else:
         y = torch.empty_like(x)
-    kda_add_rms_norm(x, residual, w, rows, D, x.dtype, eps, None if s is x else s, y, y8, scale,
-                     stream=stream)
+    kda_add_rms_norm(x, residual, w, rows, D, x.dtype, eps,
+                     None if s is x and residual is None else s, y, y8, scale, stream=stream)
     _used_on(stream, s, y, y8, scale)
     return (s, y8, scale) if quantize else (s, y)
 
@@ -1005,6 +1009,7 @@ class AddRMSNorm(torch.autograd.Function):
         return (s, y) if residual is not None else (s.view_as(s), y)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, ds, dy):
         s, w = ctx.saved_tensors
         if dy is None:
@@ -1067,6 +1072,8 @@ class Fp8Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w):
+        if w.dim() != 2 or x.shape[-1] != w.shape[1]:
+            raise ValueError(f"fp8_linear: x {tuple(x.shape)} and w {tuple(w.shape)}")
         _check_leaves(ctx, x.device)
         x2 = x.reshape(-1, x.shape[-1]).contiguous()
         w8, w_scale = quantize_fp8(w, block_rows=128)
@@ -1077,6 +1084,7 @@ class Fp8Linear(torch.autograd.Function):
         return y.view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x2, w = ctx.saved_tensors
         (M, K), N = x2.shape, w.shape[0]

@@ -87,6 +87,21 @@ def test_norm_writes_the_sum_in_place_and_both_outputs():
         kda.kda_add_rms_norm(xs, rs, w, rows, D, "bf16", 1e-6, target, yb, y8b, scb)
         assert torch.equal(target, s) and torch.equal(yb, y)
         assert torch.equal(y8b.view(torch.uint8), y8.view(torch.uint8)) and torch.equal(scb, scale)
+    for pick in (0, 1):
+        xs, rs = x.clone(), r.clone()
+        target = (xs, rs)[pick]
+        got, yb = kda.add_rms_norm(xs, w, rs, sum=target)
+        assert got is target and torch.equal(target, s) and torch.equal(yb, y)
+    both, twice = kda.add_rms_norm(x, w, x)      # the same tensor twice
+    assert torch.equal(both, x + x)
+
+
+def test_padding_behind_a_row_of_nan_is_zero():
+    x = torch.full((2, 24), float("nan"), device="cuda")
+    x[1] = 1.0
+    _, y8, _ = kda.add_rms_norm(x, torch.ones(24, device="cuda"), quantize=True)
+    assert y8.shape == (2, 32) and not y8.view(torch.uint8)[:, 24:].any()
+    assert (y8.view(torch.uint8)[:, :24] & 0x7F)[0].eq(0x7F).all()
 
 
 def test_norm_of_zero_rows_large_values_and_nan():
@@ -354,6 +369,33 @@ def test_gradients_captured_into_a_graph():
     torch.cuda.synchronize()
     for a, b in zip(out, want):
         assert torch.equal(a, b)
+
+
+def test_second_derivatives_are_refused():
+    x = randn(80, 4, 64, dtype="f32").cuda().requires_grad_()
+    w = torch.ones(64, device="cuda")
+    w2 = randn(81, 64, 64).cuda()
+    for y in (kda.residual_rms_norm(x, w)[1], kda.fp8_linear(x, w2),
+              kda.gated_linear_scan(x.view(4, 1, 64), torch.zeros(4, 1, 64, device="cuda"))[0]):
+        dy = torch.ones_like(y).requires_grad_()
+        grad, = torch.autograd.grad(y, x, dy, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            grad.sum().backward()
+
+
+@pytest.mark.parametrize("M", [5, 40, 300])
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_product_into_outputs_that_start_on_16_bytes(M, out_dtype):
+    N, K = 256, 200
+    a8, sa = kda.quantize_fp8(randn(82, M, K).cuda())
+    for rows in (1, 128):
+        b8, sb = kda.quantize_fp8(randn(83, N, K).cuda(), block_rows=rows)
+        want = kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=rows, out_dtype=DT[out_dtype])
+        skip = 16 // want.element_size()
+        buf = torch.zeros(M * N + 2 * skip, dtype=DT[out_dtype], device="cuda")
+        out = buf[skip:skip + M * N].view(M, N)
+        kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=rows, out=out)
+        assert torch.equal(out, want) and not buf[:skip].any() and not buf[-skip:].any()
 
 
 def test_a_layer_from_its_parts():

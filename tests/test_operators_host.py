@@ -33,18 +33,17 @@ def test_linear_scan_refusals():
               (dict(g=FAKE + 4), INVALID), (dict(T=-1), INVALID), (dict(B=0), INVALID),
               (dict(num_seqs=2), INVALID), (dict(H=0), INVALID), (dict(d=0), INVALID),
               (dict(H=1 << 13, d=1 << 12), INVALID), (dict(initial_state=FAKE + 8), INVALID),
-              (dict(cu_seqlens=FAKE, B=2, num_seqs=2), INVALID), (dict(dtype=7), None),
+              (dict(cu_seqlens=FAKE, B=2, num_seqs=2), INVALID),
               (dict(workspace=FAKE + 16, workspace_bytes=1 << 40), INVALID),
               (dict(cu_seqlens=FAKE, T=0x7fffffff, workspace_bytes=1 << 60), INVALID)]
-    own = [c for c in common if c[1] is not None]
-    refusals(kda.kda_linear_scan_fwd, ok, own + [
+    refusals(kda.kda_linear_scan_fwd, ok, common + [
         (dict(h=None), INVALID), (dict(final_state=FAKE + 4), INVALID),
         (dict(entry_states=FAKE + 4), INVALID)])
     bwd = dict(x=FAKE, g=FAKE, initial_state=None, dout=FAKE, dfinal_state=None,
                entry_states=None, cu_seqlens=None, B=1, T=64, num_seqs=1, H=2, d=20, dtype="f32",
                dx=FAKE, dg=FAKE, dinitial_state=None, workspace=2 * FAKE, workspace_bytes=16,
                stream=0, check=False)
-    refusals(kda.kda_linear_scan_bwd, bwd, own + [
+    refusals(kda.kda_linear_scan_bwd, bwd, common + [
         (dict(dout=None), INVALID), (dict(dx=FAKE + 2), INVALID), (dict(dg=None), INVALID),
         (dict(workspace_bytes=1 << 40, dfinal_state=FAKE, dinitial_state=FAKE), INVALID),
         (dict(workspace_bytes=1 << 40, initial_state=FAKE, dinitial_state=FAKE), INVALID)])
@@ -130,6 +129,20 @@ def test_wrappers_refuse_shapes_the_library_would_misread():
         kda.fp8_matmul(a8, sa, b8, sb, b_block_rows=1)
     with pytest.raises(ValueError, match="float8"):
         kda.kda_fp8_matmul(a8.float(), sa, b8, sb, 3, 5, 32, 128, "f32", torch.zeros(3, 5))
+    with pytest.raises(ValueError, match="fp8_linear"):   # (rows of 112 bytes both)
+        kda.fp8_linear(torch.zeros(2, 97), torch.zeros(8, 112))
+
+
+def test_wrappers_refuse_tensors_that_are_not_on_a_gpu():
+    x, g, w = torch.zeros(8, 2, 4), torch.zeros(8, 2, 4), torch.ones(8)
+    y = x.view(8, 8)
+    a8, sa = torch.zeros(3, 32, dtype=torch.uint8), torch.zeros(1, 3)
+    for call in (lambda: kda.linear_scan(x, g), lambda: kda.linear_scan_bwd(x, g, x),
+                 lambda: kda.linear_scan_step(x, g, x), lambda: kda.add_rms_norm(y, w),
+                 lambda: kda.add_rms_norm_bwd(y, w, y), lambda: kda.quantize_fp8(y),
+                 lambda: kda.fp8_matmul(a8, sa, a8, sa, b_block_rows=1)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call()
 
 
 def test_scan_reference_is_the_explicit_sum_and_its_gradient_a_difference():
