@@ -26,6 +26,12 @@
 // With few tiles the K blocks are split over a cluster of up to 8 CTAs, which
 // add their partial tiles through distributed shared memory in a fixed order.
 //
+// Measured on a B200: 8192 x 4096 x 4096 in bf16 134 us (2.05 PFLOP/s; 158 in a
+// long run under the power cap), with a scale per row on both sides 4096 x 4096 x
+// 4099 in fp32 111 us (1.24 PFLOP/s); a block's products and sums take 1000 cycles
+// and the products alone 512.  Giving each half of a last, part-filled round of
+// tiles to a CTA of its own gained nothing: a half takes a block as long.
+//
 // Every wait is bounded; a tile whose waits gave up is written as NaN.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -12,6 +12,10 @@
 // without bank conflicts, once for the maximum and once more for the codes (so
 // that six CTAs fit on an SM instead of three); the codes go through shared
 // memory too, so that eight lanes write 128 bytes of a row of the result.
+//
+// Measured on a B200 (of the copy rate of 6.53 TB/s), bf16: 12288 x 4096 by 128 x
+// 128 blocks 27.5 us (84 %); 4099 x 4096 transposed 11.5 us (68 %; 14.4 with codes
+// written by columns and three CTAs per SM).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

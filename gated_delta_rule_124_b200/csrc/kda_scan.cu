@@ -43,6 +43,11 @@
 // the same look-back runs from the right for e, and h_{t-1} is recomputed
 // inside each tile from the tile's entry state, which the forward keeps (one
 // fp32 row per 64 tokens).  x, g, dout in and dx, dg out, each once.
+//
+// Measured on a B200 (of the copy rate of 6.53 TB/s), bf16: forward of 65536 x
+// 4096 channels 424 us (77 %; 593 in fp32, 83 %), backward 710 (81 %); 4096 x
+// 4096 35 and 53; 262144 x 128 94 and 134; a step of 256 x 4096 2.5 us.  Against
+// the copy rate the look-back costs most: without it the long forward takes 350.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -414,7 +419,7 @@ struct Maps {
 
 // Tiles of a group.  Where few channels leave many tiles of one sequence on the
 // device at once, groups keep the look-back short (262144 x 128: 94 us, 244
-// without); else the maps and exit states of single tiles do (65536 x 4096: 420
+// without); else the maps and exit states of single tiles do (65536 x 4096: 424
 // us, 448 with groups).
 constexpr int kGroup = 6;
 inline int group_of(int ctiles) { return ctiles < 8 ? kGroup : 1; }
@@ -694,7 +699,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* __restrict__ x,
 
 // The workspace of a scan: [0, 256) status word, then the ticket (256 bytes)
 // and one 64-bit word per (tile, channel) and per (group of tiles, channel) --
-// none of these when the tokens fit in one tile -- and, for a backward without entry states, those.
+// none of these when the tokens fit in one tile -- and, for a backward without
+// entry states, those.
 struct ScanSpace {
     uint32_t* status;
     uint32_t* ticket;
@@ -749,7 +755,7 @@ template <typename T>
 cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, cudaStream_t st) {
     // rows of C channels start on a 16-byte (fp32) or 8-byte (bf16) boundary
     // when C is a multiple of 4; other sizes take one channel per lane, and
-    // four times the rows
+    // four times the rows (100000 x 155 bf16: 56 us, 93 with eight rows)
     if (a.C % 4 != 0) return run_scan<1, 32, T>(a, s, backward, st);
     return run_scan<4, 8, T>(a, s, backward, st);
 }

@@ -271,6 +271,16 @@ def test_product_matches_fp64(M, N, K, block, out_dtype):
     assert torch.isnan(out[M:]).all()     # rows behind the last one stay as they were
 
 
+@pytest.mark.parametrize("block,out_dtype", [(128, "bf16"), (1, "f32")])
+@pytest.mark.parametrize("M,N,K", [(1700, 3100, 300), (128 * 16, 256 * 10, 256), (40 * 128, 1024, 130),
+                                   (9500, 520, 128)])
+def test_product_of_a_full_round_of_tiles_and_a_part(M, N, K, block, out_dtype):
+    """160 to 225 tiles of 128 x 256 on 148 SMs."""
+    a8, sa, b8, sb = operands(M + N, M, N, K, block)
+    out = kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out_dtype=DT[out_dtype])
+    check_product(out, a8, sa, b8, sb, K, block, out_dtype)
+
+
 @pytest.mark.parametrize("M", [16, 300, 1500])
 def test_product_is_the_same_every_time(M):
     args = operands(3, M, 1024, 2048, 128)
