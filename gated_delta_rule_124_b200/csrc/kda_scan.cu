@@ -45,9 +45,10 @@
 // fp32 row per 64 tokens).  x, g, dout in and dx, dg out, each once.
 //
 // Measured on a B200 (of the copy rate of 6.53 TB/s), bf16: forward of 65536 x
-// 4096 channels 424 us (77 %; 593 in fp32, 83 %), backward 710 (81 %); 4096 x
-// 4096 35 and 53; 262144 x 128 94 and 134; a step of 256 x 4096 2.5 us.  Against
-// the copy rate the look-back costs most: without it the long forward takes 350.
+// 4096 channels 415 us (79 %; 576 in fp32, 86 %), backward 667 (86 %; fp32 813);
+// 4096 x 4096 33 and 53; 262144 x 128 93 and 130; a step of 256 x 4096 2.5 us.
+// Against the copy rate the look-back costs most: without it the long forward
+// took 350.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -87,6 +88,14 @@ struct ScanArgs {
     int tiles, ctiles;      // of the launched kernel's size
 };
 
+// How x, g and dout are loaded (every element once): past L1, or with L1's and
+// L2's ordinary policy, which is better for the backward pass where rows are long
+// (65536 tokens, us, past L1 and ordinary: backward of 4096 channels 701 and 665,
+// fp32 870 and 809, of 1024 198 and 206; forward of 4096 414 and 425, of 1024 138
+// and 145).  Stores go past L1.
+enum class Policy { kPastL1, kOrdinary };
+constexpr int kLongRow = 2048;
+
 // Four channels (VEC = 4) or one (VEC = 1) of a row; fp32 or bf16.
 template <int VEC, typename T>
 struct Raw;
@@ -94,14 +103,30 @@ template <>
 struct Raw<4, float> {
     float4 v;
     __device__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ void load(const float* p) { v = __ldcs(reinterpret_cast<const float4*>(p)); }
+    template <Policy P>
+    __device__ void load(const float* p) {
+        if (P == Policy::kOrdinary)
+            v = __ldg(reinterpret_cast<const float4*>(p));
+        else
+            asm("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                : "l"(p));
+    }
     __device__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
 };
 template <>
 struct Raw<4, __nv_bfloat16> {
     uint2 v;
     __device__ void zero() { v = make_uint2(0u, 0u); }
-    __device__ void load(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint2*>(p)); }
+    template <Policy P>
+    __device__ void load(const __nv_bfloat16* p) {
+        if (P == Policy::kOrdinary)
+            v = __ldg(reinterpret_cast<const uint2*>(p));
+        else
+            asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                : "=r"(v.x), "=r"(v.y)
+                : "l"(p));
+    }
     __device__ void get(float (&o)[4]) const {
         o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xFFFF0000u);
         o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
@@ -111,20 +136,23 @@ template <typename T>
 struct Raw<1, T> {
     T v;
     __device__ void zero() { v = from_f32<T>(0.f); }
+    template <Policy>
     __device__ void load(const T* p) { v = *p; }
     __device__ void get(float (&o)[1]) const { o[0] = to_f32(v); }
 };
 
 __device__ __forceinline__ void put(float* p, const float (&o)[4]) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(o[0], o[1], o[2], o[3]));
+    asm volatile("st.global.L1::no_allocate.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(o[0]),
+                 "f"(o[1]), "f"(o[2]), "f"(o[3])
+                 : "memory");
 }
 __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&o)[4]) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]);
     const __nv_bfloat162 b = __floats2bfloat162_rn(o[2], o[3]);
-    uint2 u;
-    u.x = *reinterpret_cast<const uint32_t*>(&a);
-    u.y = *reinterpret_cast<const uint32_t*>(&b);
-    __stcs(reinterpret_cast<uint2*>(p), u);
+    asm volatile("st.global.L1::no_allocate.v2.u32 [%0], {%1, %2};" ::"l"(p),
+                 "r"(*reinterpret_cast<const uint32_t*>(&a)),
+                 "r"(*reinterpret_cast<const uint32_t*>(&b))
+                 : "memory");
 }
 template <typename T>
 __device__ __forceinline__ void put(T* p, const float (&o)[1]) { *p = from_f32<T>(o[0]); }
@@ -360,16 +388,16 @@ __device__ __forceinline__ int next_tile(const ScanArgs& a) {
 // A warp's rows of a tile in registers.  Lanes beyond the last channel load the
 // last ones again (they store nothing); rows beyond the last token hold zeros,
 // which change no state.
-template <int VEC, int R, typename U>
+template <Policy P, int VEC, int R, typename U>
 __device__ __forceinline__ void load_rows(Raw<VEC, U> (&v)[R], const U* p, size_t C, int rows) {
     if (rows >= R) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) v[r].load(p + r * C);
+        for (int r = 0; r < R; ++r) v[r].template load<P>(p + r * C);
     } else {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             v[r].zero();
-            if (r < rows) v[r].load(p + r * C);
+            if (r < rows) v[r].template load<P>(p + r * C);
         }
     }
 }
@@ -418,32 +446,43 @@ struct Maps {
 };
 
 // Tiles of a group.  Where few channels leave many tiles of one sequence on the
-// device at once, groups keep the look-back short (262144 x 128: 94 us, 244
-// without); else the maps and exit states of single tiles do (65536 x 4096: 424
+// device at once, groups keep the look-back short (262144 x 128: 93 us, 244
+// without); else the maps and exit states of single tiles do (65536 x 4096: 415
 // us, 448 with groups).
 constexpr int kGroup = 6;
 inline int group_of(int ctiles) { return ctiles < 8 ? kGroup : 1; }
 
+// A thread's gates between the two passes over its rows, where a lane has one
+// channel (its 32 rows are more registers than there are: 100000 x 155 bf16 58 ->
+// 54 us; with four channels they stay in registers, 415 us against 430).
+template <int VEC, int R>
+struct KeptGates {
+    float v[VEC == 1 ? R : 1][VEC == 1 ? kThreads : 1];
+};
+
 // kBounds: sequences begin or end in the tile, or the tokens do.
 template <int VEC, int R, int GROUP, typename T, bool kBounds>
 __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Maps<VEC>& s_maps,
-                                         const Bounds<8 * R>& s_bounds, const Raw<VEC, T> (&xr)[R],
+                                         const Bounds<8 * R>& s_bounds, KeptGates<VEC, R>& s_gates,
+                                         const Raw<VEC, T> (&xr)[R],
                                          const Raw<VEC, float> (&gr)[R], int c, bool mine) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = tile * 8 * R;
     const size_t C = a.C;
     // the map of this warp's rows
-    float al[R][VEC];
+    float al[VEC == 1 ? 1 : R][VEC];  // (one channel: the present row's)
     {
         float G[VEC], b[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) G[j] = b[j] = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            constexpr bool kKeep = VEC == 1;
+            const int k = kKeep ? 0 : r;
             float gv[VEC], xv[VEC];
             gr[r].get(gv);
             xr[r].get(xv);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) al[r][j] = gate(gv[j], G[j]);
+            for (int j = 0; j < VEC; ++j) al[k][j] = gate(gv[j], G[j]);
             const int first = kBounds ? s_bounds.first_of[w * R + r] : -1;
             if (kBounds && first >= 0) {
                 state_of<VEC>(a.h0, first, C, c, b);
@@ -451,14 +490,15 @@ __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Ma
                 for (int j = 0; j < VEC; ++j) G[j] = -INFINITY;
             }
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[r][j], b[j], xv[j]);
+            for (int j = 0; j < VEC; ++j) b[j] = fmaf(al[k][j], b[j], xv[j]);
             // from here on a first row's al is its state: initial_state is read
             // before this tile publishes anything, so that final_state may be
             // the same buffer
             if (kBounds && first >= 0) {
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) al[r][j] = b[j];
+                for (int j = 0; j < VEC; ++j) al[k][j] = b[j];
             }
+            if (kKeep) s_gates.v[kKeep ? r : 0][kKeep ? threadIdx.x : 0] = al[0][0];
         }
         s_maps.set(w, lane, G, b);
     }
@@ -497,11 +537,14 @@ __device__ __forceinline__ void fwd_tile(const ScanArgs& a, int tile, int c0, Ma
     for (int r = 0; r < R; ++r) {
         if (kBounds && t0 + w * R + r >= a.total) return;
         const int first = kBounds ? s_bounds.first_of[w * R + r] : -1;
+        constexpr bool kKeep = VEC == 1;
+        const int k = kKeep ? 0 : r;
+        if (kKeep) al[0][0] = s_gates.v[kKeep ? r : 0][kKeep ? threadIdx.x : 0];
         float xv[VEC];
         xr[r].get(xv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-            h[j] = kBounds && first >= 0 ? al[r][j] : fmaf(al[r][j], h[j], xv[j]);
+            h[j] = kBounds && first >= 0 ? al[k][j] : fmaf(al[k][j], h[j], xv[j]);
         if (a.h) put(out + r * C, h);
         const int last = kBounds ? s_bounds.last_of[w * R + r] : -1;
         if (kBounds && last >= 0 && a.final_state) {
@@ -515,6 +558,7 @@ template <int VEC, int R, int GROUP, typename T>
 __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs a) {
     constexpr int CT = 32 * VEC;  // channels of a tile
     __shared__ __align__(16) Maps<VEC> s_maps;
+    __shared__ KeptGates<VEC, R> s_gates;
     __shared__ Bounds<8 * R> s_bounds;
     const int task = next_tile(a), tile = task / a.ctiles, c0 = (task % a.ctiles) * CT;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -522,17 +566,18 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs a)
     const int c = mine ? c0 + lane * VEC : a.C - VEC;
     Raw<VEC, T> xr[R];
     Raw<VEC, float> gr[R];
-    load_rows(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C, a.total - t);
-    load_rows(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
+    load_rows<Policy::kPastL1>(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C,
+                               a.total - t);
+    load_rows<Policy::kPastL1>(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
     find_bounds(a, tile * 8 * R, s_bounds);
     if (tile == 0) {
         if (c0 == 0) report_status(a);
         pass_empty(a, a.h0, a.final_state, c0, min(CT, a.C - c0));
     }
     if (s_bounds.plain)
-        fwd_tile<VEC, R, GROUP, T, false>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+        fwd_tile<VEC, R, GROUP, T, false>(a, tile, c0, s_maps, s_bounds, s_gates, xr, gr, c, mine);
     else
-        fwd_tile<VEC, R, GROUP, T, true>(a, tile, c0, s_maps, s_bounds, xr, gr, c, mine);
+        fwd_tile<VEC, R, GROUP, T, true>(a, tile, c0, s_maps, s_bounds, s_gates, xr, gr, c, mine);
 }
 
 template <int VEC, int R, int GROUP, typename T, bool kBounds>
@@ -648,7 +693,7 @@ __device__ __forceinline__ void bwd_tile(const ScanArgs& a, int tile, int c0, Ma
     }
 }
 
-template <int VEC, int R, int GROUP, typename T>
+template <int VEC, int R, int GROUP, Policy P, typename T>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a) {
     constexpr int CT = 32 * VEC;
     __shared__ __align__(16) Maps<VEC> s_maps, s_back;
@@ -660,9 +705,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanArgs a)
     const int c = mine ? c0 + lane * VEC : a.C - VEC;
     Raw<VEC, T> xr[R], dr[R];
     Raw<VEC, float> gr[R];
-    load_rows(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
-    load_rows(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C, a.total - t);
-    load_rows(dr, static_cast<const T*>(a.dout) + (size_t)t * a.C + c, a.C, a.total - t);
+    load_rows<P>(gr, a.g + (size_t)t * a.C + c, a.C, a.total - t);
+    load_rows<P>(xr, static_cast<const T*>(a.x) + (size_t)t * a.C + c, a.C, a.total - t);
+    load_rows<P>(dr, static_cast<const T*>(a.dout) + (size_t)t * a.C + c, a.C, a.total - t);
     find_bounds(a, tile * 8 * R, s_bounds);
     if (tile == a.tiles - 1) {
         if (c0 == 0) report_status(a);
@@ -684,9 +729,9 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* __restrict__ x,
     if (i >= n) return;
     Raw<VEC, T> xr;
     Raw<VEC, float> gr, sr;
-    xr.load(x + i);
-    gr.load(g + i);
-    sr.load(state_in + i);
+    xr.template load<Policy::kPastL1>(x + i);
+    gr.template load<Policy::kPastL1>(g + i);
+    sr.v = *reinterpret_cast<const decltype(sr.v)*>(state_in + i);  // (may be state_out)
     float xv[VEC], gv[VEC], s[VEC];
     xr.get(xv);
     gr.get(gv);
@@ -743,10 +788,14 @@ cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t
             cudaMemsetAsync(s.ticket, 0xFF, kAlign + sizeof(uint64_t) * a.C * (size_t)words, st);
         if (e != cudaSuccess) return e;
     }
+    constexpr Policy kPast = Policy::kPastL1;
     const bool one = group_of(a.ctiles) == 1;
-    const auto kernel =
-        backward ? (one ? scan_bwd_kernel<VEC, R, 1, T> : scan_bwd_kernel<VEC, R, kGroup, T>)
-                 : (one ? scan_fwd_kernel<VEC, R, 1, T> : scan_fwd_kernel<VEC, R, kGroup, T>);
+    auto kernel = backward ? (one ? scan_bwd_kernel<VEC, R, 1, kPast, T>
+                                  : scan_bwd_kernel<VEC, R, kGroup, kPast, T>)
+                           : (one ? scan_fwd_kernel<VEC, R, 1, T>
+                                  : scan_fwd_kernel<VEC, R, kGroup, T>);
+    if constexpr (VEC == 4)
+        if (backward && a.C >= kLongRow) kernel = scan_bwd_kernel<VEC, R, 1, Policy::kOrdinary, T>;
     kernel<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
@@ -755,7 +804,7 @@ template <typename T>
 cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, cudaStream_t st) {
     // rows of C channels start on a 16-byte (fp32) or 8-byte (bf16) boundary
     // when C is a multiple of 4; other sizes take one channel per lane, and
-    // four times the rows (100000 x 155 bf16: 56 us, 93 with eight rows)
+    // four times the rows (100000 x 155 bf16: 54 us, 93 with eight rows)
     if (a.C % 4 != 0) return run_scan<1, 32, T>(a, s, backward, st);
     return run_scan<4, 8, T>(a, s, backward, st);
 }
