@@ -39,7 +39,7 @@ template <>
 struct Vec8<__nv_bfloat16> {
     uint4 u;
     __device__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
     __device__ void get(float (&x)[8]) const {
         const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -54,8 +54,8 @@ struct Vec8<float> {
     float4 a, b;
     __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ void load(const float* p) {
-        a = __ldcs(reinterpret_cast<const float4*>(p));
-        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ void get(float (&x)[8]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;

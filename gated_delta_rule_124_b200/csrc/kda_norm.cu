@@ -20,9 +20,10 @@
 // kernel, in a fixed order.
 //
 // Measured on a B200 (of the copy rate of 6.53 TB/s), bf16: 16391 x 4096 with a
-// residual to 8 bits 77 us (94 %), 16 rows 2.8; backward of 8192 x 4096 47 us (87
-// %, 4 of it the second kernel).  Without the request of the next row ahead of the
-// reduction a row's loads would wait for the row before.
+// residual to 8 bits 73 us (98 %; 77 with loads marked as streaming), 16 rows 2.8;
+// backward of 8192 x 4096 46 us (89 %, 4 of it the second kernel).  Without the
+// request of the next row ahead of the reduction a row's loads would wait for the
+// row before.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
