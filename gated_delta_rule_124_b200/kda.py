@@ -227,6 +227,8 @@ def _args(what, *pairs):
 # this torch offers that).
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+# The current device, once there are tensors on one.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _enqueue(name, device, stream, check, *args) -> int:
@@ -240,7 +242,7 @@ def _enqueue(name, device, stream, check, *args) -> int:
         stream = _current_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         return _ret(fn(*args, stream), name, check)
     with torch.cuda.device(device):
         return _ret(fn(*args, stream), name, check)
