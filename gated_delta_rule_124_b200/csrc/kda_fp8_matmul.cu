@@ -677,6 +677,13 @@ cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cu
 // 12.0 (16.7 unsplit), 2 ways 15.2 (16.9), unsplit 17.6; 256 rows unsplit 22.3
 // (29.6 with 128) and 134 (174).  With a scale per row of B 0.53 and 0.83
 // (4096 x 4096 x 4099: 110 with 256 rows, 124 with 128).
+// The CTAs of a cluster share one of the device's groups of SMs, whose sizes four
+// and eight do not divide: 148 SMs hold 33 clusters of four and 15 of eight (as
+// the occupancy query says; 16 tiles split eight ways took two rounds, 15.6 for 64
+// x 2048 x 4096 against 9.5 split four ways).
+int clusters(int sms, int split) {
+    return split == 8 ? sms * 15 / 148 : split == 4 ? sms * 33 / 148 : sms / split;
+}
 void choose(int M, int N, int KB, bool b_rows, int sms, int* bn, int* split) {
     double best = 0.;
     for (int n = 128; n <= 256; n += 128) {
@@ -684,7 +691,7 @@ void choose(int M, int N, int KB, bool b_rows, int sms, int* bn, int* split) {
         const double join = n == 128 ? 4. : 7.;
         const double tiles = ((M + kRowsA - 1) / kRowsA) * (double)((N + n - 1) / n);
         for (int s = 1; s <= kMaxSplit && s <= KB; s *= 2) {
-            const double rounds = std::ceil(tiles / (sms / s));
+            const double rounds = std::ceil(tiles / clusters(sms, s));
             const double t = rounds * ((KB + s - 1) / s * block + (s > 1 ? join : 0.));
             if (best == 0. || t < best) {
                 best = t;
@@ -730,11 +737,12 @@ cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* 
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // few rows: the kernel without stages, while it takes a round or two
-    // (4096 x 4096, 8 and 16 rows of A: 6.2 and 9.8 us against 10.2 and 10.3 here;
-    // 12288 x 4096: 15.0 and 24.7 against 19.3)
+    // few rows: the kernel without stages, with up to 16 rows while it takes one
+    // round (4096 x 4096, 8 and 16 rows of A: 6.6 and 9.8 us against 9.7 and 10.0
+    // here; 4096 x 2048 4.7 and 6.5 against 8.0 and 8.1; 8192 x 4096 11.1 and 17.7
+    // against 13.5 and 14.0; 2048 x 16384, 8 rows: 15.6 against 16.7)
     const long long rounds = ((long long)N + 32 * sms - 1) / (32 * sms) * ((K + 4095) / 4096);
-    if (M <= 8 ? K <= 8192 : M <= 16 && rounds <= 2)
+    if (M <= 8 ? K <= 8192 : M <= 16 && rounds <= 1)
         return launch_fp8_small(a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, st);
     int bn = 0, split = 0;
     choose(M, N, blocks128(K), b_rows, sms, &bn, &split);
