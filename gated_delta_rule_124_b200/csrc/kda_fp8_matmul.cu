@@ -677,12 +677,15 @@ cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cu
 // 12.0 (16.7 unsplit), 2 ways 15.2 (16.9), unsplit 17.6; 256 rows unsplit 22.3
 // (29.6 with 128) and 134 (174).  With a scale per row of B 0.53 and 0.83
 // (4096 x 4096 x 4099: 110 with 256 rows, 124 with 128).
-// The CTAs of a cluster share one of the device's groups of SMs, whose sizes four
-// and eight do not divide: 148 SMs hold 33 clusters of four and 15 of eight (as
-// the occupancy query says; 16 tiles split eight ways took two rounds, 15.6 for 64
-// x 2048 x 4096 against 9.5 split four ways).
+// The CTAs of a cluster share one of the device's groups of SMs, whose sizes few
+// numbers divide: 148 SMs hold 45 clusters of three, 33 of four and 15 of eight (the
+// occupancy query's answers; 16 tiles split eight ways took two rounds, 15.6 for 64
+// x 2048 x 4096 against 9.5 split four ways; 64 x 5120 x 4096 11.2 split three ways,
+// 12.6 two).  Five to seven ways are left out: a tenth better for one shape in
+// fifteen, up to 4 % worse than four or eight for others.
+constexpr int kSplits[] = {1, 2, 3, 4, kMaxSplit};
 int clusters(int sms, int split) {
-    return split == 8 ? sms * 15 / 148 : split == 4 ? sms * 33 / 148 : sms / split;
+    return sms * (split == 3 ? 45 : split == 4 ? 33 : split == 8 ? 15 : 148 / split) / 148;
 }
 void choose(int M, int N, int KB, bool b_rows, int sms, int* bn, int* split) {
     double best = 0.;
@@ -690,7 +693,8 @@ void choose(int M, int N, int KB, bool b_rows, int sms, int* bn, int* split) {
         const double block = b_rows ? (n == 128 ? 0.53 : 0.83) : (n == 128 ? 0.39 : 0.54);
         const double join = n == 128 ? 4. : 7.;
         const double tiles = ((M + kRowsA - 1) / kRowsA) * (double)((N + n - 1) / n);
-        for (int s = 1; s <= kMaxSplit && s <= KB; s *= 2) {
+        for (const int s : kSplits) {
+            if (s > KB) break;
             const double rounds = std::ceil(tiles / clusters(sms, s));
             const double t = rounds * ((KB + s - 1) / s * block + (s > 1 ? join : 0.));
             if (best == 0. || t < best) {

@@ -281,6 +281,16 @@ def test_product_of_a_full_round_of_tiles_and_a_part(M, N, K, block, out_dtype):
     check_product(out, a8, sa, b8, sb, K, block, out_dtype)
 
 
+@pytest.mark.parametrize("block", [128, 1])
+@pytest.mark.parametrize("M,N,K", [(20, 1000, 4100), (70, 2050, 4096), (20, 5120, 4096),
+                                   (130, 2500, 4096), (200, 4096, 3000), (9, 300, 9000)])
+def test_product_of_a_split_k(M, N, K, block):
+    """Eight, four, three and two ways."""
+    a8, sa, b8, sb = operands(M + N, M, N, K, block)
+    out = kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out_dtype=torch.float32)
+    check_product(out, a8, sa, b8, sb, K, block, "f32")
+
+
 @pytest.mark.parametrize("M", [16, 300, 1500])
 def test_product_is_the_same_every_time(M):
     args = operands(3, M, 1024, 2048, 128)
