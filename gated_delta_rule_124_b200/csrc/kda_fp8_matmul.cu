@@ -619,6 +619,194 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, NB * 128);
 }
 
+// Up to 16 rows of A: the operands change places, so that the 128 lanes of a product
+// are rows of B (a weight, read once: the call is bound by HBM) and its 16 columns
+// the rows of A.  A CTA has 128 rows of B and a share of the K blocks, two CTAs an
+// SM, each with five blocks' loads in flight; warp 0 loads, warp 1 issues the
+// products, warps 2-5 take a row of B a thread through its blocks, the scales of the
+// next four requested ahead.  16 x 12288 x 4096 15.2 us (7.7 at the copy rate; with
+// the plan above 21.3), 16 x 8192 x 4096 12.3 (14.0); an SM takes in about 60 bytes
+// a ns this way, with more stages or two blocks a stage no more.
+constexpr int kFewThreads = 192;
+constexpr int kFewRows = 16;                                // of A
+constexpr uint32_t kFewStage = kTileA + kFewRows * 128;
+constexpr int kFewStages = 5;
+constexpr int kFewBuffers = 4;                              // of tensor memory
+constexpr uint32_t kFewSmem = 1024 + kFewStages * kFewStage;
+static_assert(kFewStages * kFewStage >= kFewRows * kRowsA * 4, "a partial tile fits the stages");
+
+template <bool kRowScales>
+__global__ void __launch_bounds__(kFewThreads)
+    fp8_few_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
+                   const MatmulArgs a) {
+    constexpr int ST = kFewStages, NB = kFewBuffers, MP = kFewRows;
+    extern __shared__ uint8_t mm_smem[];
+    __shared__ __align__(8) uint64_t full[ST], empty[ST], tfull[NB], tempty[NB];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_fail;
+    uint8_t* stages = mm_smem + ((1024u - (smem_u32(mm_smem) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % a.split, n0 = blockIdx.x / a.split * kRowsA;
+    const int kb0 = static_cast<int>((long long)rank * a.KB / a.split);
+    const int kb1 = static_cast<int>((long long)(rank + 1) * a.KB / a.split);
+
+    if (warp == 1) {
+        tmem_alloc(&s_tmem, NB * MP);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        s_fail = 0;
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4);
+        }
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* fail = &s_fail;
+    float* part = reinterpret_cast<float*>(stages);  // [rows of A][128], once the stages are read
+
+    if (warp == 0) {
+        if (elect_one()) {
+            int it = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % ST;
+                if (*fail || !wait(&empty[s], ((it / ST) & 1) ^ 1)) {
+                    *fail = 1;
+                    break;
+                }
+                uint8_t* st = stages + s * kFewStage;
+                mbar_arrive_expect_tx(&full[s], kFewStage);
+                tma_load_2d(st, &tmw, &full[s], kb * 128, n0);
+                tma_load_2d(st + kTileA, &tmx, &full[s], kb * 128, 0);
+            }
+            // loads in flight land before the stages are written again (a no-op
+            // unless a wait gave up: the products have waited for every load)
+            for (int s = 0; s < ST && s < it; ++s) wait(&full[s], ((it - 1 - s) / ST) & 1);
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            constexpr uint32_t id = idesc_e4m3_f32(kRowsA, MP);
+            int it = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % ST, b = it % NB;
+                if (!wait(&full[s], (it / ST) & 1) || !wait(&tempty[b], ((it / NB) & 1) ^ 1)) {
+                    *fail = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sA = smem_u32(stages + s * kFewStage);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f8(tmem + b * MP, sdesc_sw128(sA + k * 32, 16, 1024),
+                           sdesc_sw128(sA + kTileA + k * 32, 16, 1024), id, k > 0);
+                mma_commit(&tfull[b]);
+                mma_commit(&empty[s]);
+            }
+            // no product is in flight when the tensor memory goes back
+            if (it > 0) wait(&tfull[(it - 1) % NB], ((it - 1) / NB) & 1);
+        }
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21);
+        // a block's scales: lane m has row m's of A, every lane its row's of B
+        const int nb = kRowScales ? n0 + row : n0 / 128;
+        auto scale_a = [&](int kb) {
+            return kb < kb1 && lane < a.M ? a.sa[(size_t)kb * a.M + lane] : 0.f;
+        };
+        auto scale_b = [&](int kb) {
+            return kb < kb1 && nb < a.NB ? a.sb[(size_t)kb * a.NB + nb] : 0.f;
+        };
+        float xa[NB], xb[NB];
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+            xa[u] = scale_a(kb0 + u);
+            xb[u] = scale_b(kb0 + u);
+        }
+        float acc[MP];
+#pragma unroll
+        for (int m = 0; m < MP; ++m) acc[m] = 0.f;
+        bool ok = true;
+        for (int base = kb0; base < kb1 && ok; base += NB) {
+#pragma unroll
+            for (int u = 0; u < NB; ++u) {  // block u of these is in buffer u
+                const int kb = base + u, it = kb - kb0;
+                if (kb >= kb1 || !ok) break;
+                ok = __all_sync(0xffffffffu, wait(&tfull[u], (it / NB) & 1));
+                if (!ok) {
+                    *fail = 1;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t r[16];
+                tmem_ld16(tq + u * MP, r);
+                tmem_wait(r);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[u]);
+#pragma unroll
+                for (int m = 0; m < MP; ++m) {
+                    const float s = __shfl_sync(0xffffffffu, xa[u], m) * xb[u];
+                    acc[m] = fmaf(__uint_as_float(r[m]), s, acc[m]);
+                }
+                xa[u] = scale_a(kb + NB);
+                xb[u] = scale_b(kb + NB);
+            }
+        }
+        // NaN instead of a sum that lacks blocks
+        if (!ok)
+#pragma unroll
+            for (int m = 0; m < MP; ++m) acc[m] = __int_as_float(0x7FFFFFFF);
+        if (a.split == 1) {
+            if (n0 + row < a.N) {
+#pragma unroll
+                for (int m = 0; m < MP; ++m) {
+                    if (m >= a.M) break;
+                    const size_t o = (size_t)m * a.N + n0 + row;
+                    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(acc[m]);
+                    else static_cast<float*>(a.out)[o] = acc[m];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < MP; ++m)
+                if (m < a.M) part[m * kRowsA + row] = acc[m];
+        }
+    }
+    __syncwarp();
+    if (a.split > 1) {
+        cluster_sync();
+        // this CTA's share of the tile, neighbouring rows of B in neighbouring lanes
+        const int all = a.M * (kRowsA / 4);
+        const int e0 = all * rank / a.split, e1 = all * (rank + 1) / a.split;
+        for (int e = e0 + threadIdx.x; e < e1; e += kFewThreads) {
+            const int m = e / (kRowsA / 4), c = e % (kRowsA / 4) * 4;
+            if (n0 + c >= a.N) continue;
+            const uint32_t addr = smem_u32(part) + (m * kRowsA + c) * 4;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+            for (int p = 0; p < a.split; ++p) {
+                const float4 x = peer_f32x4(addr, p);
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            }
+            write4(a, v, (size_t)m * a.N + n0 + c, a.N - n0 - c);
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while others read its part
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, NB * MP);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void* ptr = nullptr;
@@ -647,27 +835,35 @@ bool map_bytes(CUtensorMap* m, const void* base, int rows, int K, int box) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch of `ctas` CTAs in clusters of `split`.
+template <typename F>
+cudaError_t launch(F kernel, int ctas, int threads, uint32_t smem, int split, cudaStream_t st,
+                   const CUtensorMap& m0, const CUtensorMap& m1, const MatmulArgs& a) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, m0, m1, a);
+}
+
 template <int BN, bool kRowScales>
 cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cudaStream_t st) {
     using P = Plan<BN>;
     CUtensorMap tma, tmb;
     if (!map_bytes(&tma, a8, a.M, K, kRowsA) || !map_bytes(&tmb, b8, a.N, K, BN))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(
-        fp8_matmul_kernel<BN, kRowScales>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.split > 1 ? a.tiles * a.split : a.tiles < sms ? a.tiles : sms);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = P::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<BN, kRowScales>, tma, tmb, a);
+    const int ctas = a.split > 1 ? a.tiles * a.split : a.tiles < sms ? a.tiles : sms;
+    return launch(fp8_matmul_kernel<BN, kRowScales>, ctas, kThreads, P::kSmem, a.split, st, tma, tmb, a);
 }
 
 // Rows of B per tile and the split of K: the pair with the least time by a model
@@ -706,6 +902,25 @@ void choose(int M, int N, int KB, bool b_rows, int sms, int* bn, int* split) {
     }
 }
 
+// Shares of K: two CTAs an SM where there are few tiles (K = 4096, 16 rows: 32 tiles
+// split 4 and 8 ways 9.3 and 9.4 us, unsplit 13.2; 64 tiles 11.8 split 4 ways, 13.7
+// unsplit; 96 tiles 14.4 unsplit, 15.7 split 2 ways).
+int few_split(int tiles, int KB, int sms) {
+    if (KB < 24) return 1;
+    if (tiles <= 2 * clusters(sms, 8)) return 8;
+    if (tiles <= 2 * clusters(sms, 4)) return 4;
+    return KB >= 64 && tiles <= 2 * clusters(sms, 2) ? 2 : 1;
+}
+
+template <bool kRowScales>
+cudaError_t run_few(const void* a8, const void* b8, const MatmulArgs& a, int K, cudaStream_t st) {
+    CUtensorMap tmw, tmx;
+    if (!map_bytes(&tmw, b8, a.N, K, kRowsA) || !map_bytes(&tmx, a8, a.M, K, kFewRows))
+        return cudaErrorInvalidValue;
+    return launch(fp8_few_kernel<kRowScales>, a.tiles * a.split, kFewThreads, kFewSmem, a.split, st, tmw,
+                  tmx, a);
+}
+
 cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale, const void* b8,
                         const float* b_scale, int M, int N, int K, bool b_rows,
                         kda_dtype_t out_dt, void* out, int sms, cudaStream_t st) {
@@ -719,6 +934,12 @@ cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale,
     a.NB = b_rows ? N : blocks128(N);
     a.out_bf16 = out_dt == KDA_DTYPE_BF16;
     a.out_wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
+    if (bn == 0) {  // few rows
+        a.tiles = blocks128(N);
+        a.split = few_split(a.tiles, a.KB, sms);
+        if ((long long)a.tiles * a.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        return b_rows ? run_few<true>(a8, b8, a, K, st) : run_few<false>(a8, b8, a, K, st);
+    }
     a.ntm = static_cast<int>(((long long)M + kRowsA - 1) / kRowsA);
     a.split = split;
     const long long tiles = (long long)a.ntm * (((long long)N + bn - 1) / bn);
@@ -741,15 +962,16 @@ cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* 
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // few rows: the kernel without stages, with up to 16 rows while it takes one
-    // round (4096 x 4096, 8 and 16 rows of A: 6.6 and 9.8 us against 9.7 and 10.0
-    // here; 4096 x 2048 4.7 and 6.5 against 8.0 and 8.1; 8192 x 4096 11.1 and 17.7
-    // against 13.5 and 14.0; 2048 x 16384, 8 rows: 15.6 against 16.7)
+    // few rows: the kernel without stages while it takes a round or two (of 4096
+    // columns by 32 rows of B an SM), then the one of changed places (us, 8 and 16
+    // rows of A: 4096 x 4096 6.5 and 9.7 against 9.0 and 9.3, 4096 x 2048 4.7 and 6.5
+    // against 8.0, 8192 x 4096 11.0 and 17.5 against 11.8, 12288 x 4096 15.4 and 24.9
+    // against 14.4)
     const long long rounds = ((long long)N + 32 * sms - 1) / (32 * sms) * ((K + 4095) / 4096);
-    if (M <= 8 ? K <= 8192 : M <= 16 && rounds <= 1)
+    if (M <= 8 ? rounds <= 2 : M <= kFewRows && rounds <= 1)
         return launch_fp8_small(a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, st);
-    int bn = 0, split = 0;
-    choose(M, N, blocks128(K), b_rows, sms, &bn, &split);
+    int bn = 0, split = 1;  // bn 0: changed places
+    if (M > kFewRows) choose(M, N, blocks128(K), b_rows, sms, &bn, &split);
     return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, sms, st);
 }
 

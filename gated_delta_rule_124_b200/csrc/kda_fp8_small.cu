@@ -1,5 +1,5 @@
-// The 8-bit product of few rows (a decode step's tokens): out [M, N] = A B^T for
-// M <= 16, as in kda_fp8_matmul.cu.
+// The 8-bit product of few rows (a decode step's tokens) and a weight of a round or
+// two: out [M, N] = A B^T for M <= 16, as in kda_fp8_matmul.cu.
 //
 // B (a weight) is read once and nothing else is large: the call is bound by HBM,
 // and at its few microseconds by latency.  So everything a CTA needs is requested

@@ -283,12 +283,34 @@ def test_product_of_a_full_round_of_tiles_and_a_part(M, N, K, block, out_dtype):
 
 @pytest.mark.parametrize("block", [128, 1])
 @pytest.mark.parametrize("M,N,K", [(20, 1000, 4100), (70, 2050, 4096), (20, 5120, 4096),
-                                   (130, 2500, 4096), (200, 4096, 3000), (9, 300, 9000)])
+                                   (130, 2500, 4096), (200, 4096, 3000)])
 def test_product_of_a_split_k(M, N, K, block):
     """Eight, four, three and two ways."""
     a8, sa, b8, sb = operands(M + N, M, N, K, block)
     out = kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out_dtype=torch.float32)
     check_product(out, a8, sa, b8, sb, K, block, "f32")
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [128, 1])
+@pytest.mark.parametrize("M,N,K", [(16, 5000, 1100), (9, 300, 9000), (13, 4901, 3100),
+                                   (8, 9500, 4100), (12, 20000, 130), (1, 513, 12001),
+                                   (16, 9601, 8200), (10, 130, 5000)])
+def test_product_of_few_rows_and_a_large_weight(M, N, K, block, out_dtype):
+    """Split eight, four, two ways and not at all; the last tile and block ragged."""
+    a8, sa, b8, sb = operands(M + N, M, N, K, block)
+    out = torch.full((M + 2, N), float("nan"), dtype=DT[out_dtype], device="cuda")
+    kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out=out[:M])
+    check_product(out[:M], a8, sa, b8, sb, K, block, out_dtype)
+    assert torch.isnan(out[M:]).all()
+    first = out[:M].clone()
+    raw = b8.view(torch.uint8)
+    raw[:, K:] = 0x7F                                  # NaN codes behind the last column
+    raw[N // 2, 3] = 0x7F
+    kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out=out[:M])
+    assert torch.isnan(out[:M, N // 2]).all()
+    keep = torch.arange(N) != N // 2
+    assert torch.equal(out[:M][:, keep], first[:, keep])
 
 
 @pytest.mark.parametrize("M", [16, 300, 1500])
