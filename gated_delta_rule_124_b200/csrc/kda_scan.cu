@@ -445,12 +445,16 @@ struct Maps {
     }
 };
 
-// Tiles of a group.  Where few channels leave many tiles of one sequence on the
-// device at once, groups keep the look-back short (262144 x 128: 93 us, 244
-// without); else the maps and exit states of single tiles do (65536 x 4096: 415
-// us, 448 with groups).
-constexpr int kGroup = 6;
-inline int group_of(int ctiles) { return ctiles < 8 ? kGroup : 1; }
+// Tiles of a group: where few blocks of channels leave many tiles of one sequence on
+// the device at once, groups keep the look-back short (bf16, us, forward / backward:
+// 262144 x 128 in groups of six 93 / 129, without 244; 65536 x 512 in sixes 75 / 113,
+// in threes 73 / 109; 200000 x 1024 in sixes 375 / 602, in threes 363 / 593, without
+// 401 / 583; 65536 x 4096 in sixes 448, without 415).
+constexpr int kLongGroup = 6, kShortGroup = 3;
+inline int group_of(int vec, int ctiles, bool backward) {
+    if (ctiles <= 2) return kLongGroup;
+    return ctiles < (vec == 4 && !backward ? 16 : 8) ? kShortGroup : 1;
+}
 
 // A thread's gates between the two passes over its rows, where a lane has one
 // channel (its 32 rows are more registers than there are: 100000 x 155 bf16 58 ->
@@ -762,7 +766,7 @@ ScanSpace carve_scan(void* base, int total, int C, bool with_entry) {
     if (tiles > 1) {
         s.ticket = reinterpret_cast<uint32_t*>(p + off);
         s.words = reinterpret_cast<uint64_t*>(p + off + kAlign);
-        off = align_up(off + kAlign + sizeof(uint64_t) * (tiles + tiles / kGroup) * C);
+        off = align_up(off + kAlign + sizeof(uint64_t) * (tiles + tiles / kShortGroup) * C);
     }
     if (with_entry) {
         s.entry = reinterpret_cast<float*>(p + off);
@@ -770,6 +774,12 @@ ScanSpace carve_scan(void* base, int total, int C, bool with_entry) {
     }
     s.total_bytes = off;
     return s;
+}
+
+template <int VEC, int R, int GROUP, typename T>
+auto scan_kernel(bool backward) {
+    return backward ? scan_bwd_kernel<VEC, R, GROUP, Policy::kPastL1, T>
+                    : scan_fwd_kernel<VEC, R, GROUP, T>;
 }
 
 template <int VEC, int R, typename T>
@@ -780,20 +790,18 @@ cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t
     a.ctiles = (a.C + 32 * VEC - 1) / (32 * VEC);
     const long long grid = (long long)a.tiles * a.ctiles;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int group = group_of(VEC, a.ctiles, backward);
     if (a.tiles > 1) {
         a.ticket = s.ticket;
         a.words = s.words;
-        const int words = group_of(a.ctiles) == 1 ? a.tiles : a.tiles + a.tiles / kGroup;
+        const int words = group == 1 ? a.tiles : a.tiles + a.tiles / group;
         const cudaError_t e =
             cudaMemsetAsync(s.ticket, 0xFF, kAlign + sizeof(uint64_t) * a.C * (size_t)words, st);
         if (e != cudaSuccess) return e;
     }
-    constexpr Policy kPast = Policy::kPastL1;
-    const bool one = group_of(a.ctiles) == 1;
-    auto kernel = backward ? (one ? scan_bwd_kernel<VEC, R, 1, kPast, T>
-                                  : scan_bwd_kernel<VEC, R, kGroup, kPast, T>)
-                           : (one ? scan_fwd_kernel<VEC, R, 1, T>
-                                  : scan_fwd_kernel<VEC, R, kGroup, T>);
+    auto kernel = group == kLongGroup    ? scan_kernel<VEC, R, kLongGroup, T>(backward)
+                  : group == kShortGroup ? scan_kernel<VEC, R, kShortGroup, T>(backward)
+                                         : scan_kernel<VEC, R, 1, T>(backward);
     if constexpr (VEC == 4)
         if (backward && a.C >= kLongRow) kernel = scan_bwd_kernel<VEC, R, 1, Policy::kOrdinary, T>;
     kernel<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);

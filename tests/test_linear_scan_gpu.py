@@ -229,10 +229,12 @@ def test_long_sequence_on_few_channels():
 
 
 @pytest.mark.parametrize("T,H,d,dtype", [(30_000, 1, 128, "bf16"), (6_000, 16, 128, "bf16"),
-                                         (30_000, 1, 24, "f32"), (20_000, 1, 33, "bf16")])
+                                         (30_000, 1, 24, "f32"), (20_000, 1, 33, "bf16"),
+                                         (30_000, 4, 128, "bf16"), (20_000, 9, 128, "f32"),
+                                         (40_000, 1, 155, "f32"), (9_000, 1, 301, "bf16")])
 def test_results_have_the_same_bits_in_every_run(T, H, d, dtype):
-    """Few channels (tiles in groups), many, one channel per lane; more tiles than
-    fit on the device at once."""
+    """Few channels (tiles in groups of six and of three), many, one channel per lane;
+    more tiles than fit on the device at once."""
     lens = [T // 2 + 7, T - T // 2 - 7]
     X, G, I, D, F = cuda(*make(14, lens, H, d, dtype, -3.0))
     cu = offsets(lens)
@@ -261,7 +263,7 @@ def test_nan_and_infinity_stay_in_their_sequence_and_channel():
 
 
 @pytest.mark.parametrize("bad_gate", [float("nan"), 3e38])
-@pytest.mark.parametrize("C", [8, 7, 128, 1100])
+@pytest.mark.parametrize("C", [8, 7, 128, 400, 1100, 2500])
 def test_a_nan_gate_stays_in_its_sequence(C, bad_gate):
     """Sequences that begin inside the tile, and the group of tiles, of the NaN."""
     lens = [90, 20, 200, 1000, 700, 300, 1]
@@ -308,11 +310,12 @@ def test_gates_beyond_the_range_of_exp():
     assert (h[0] == 2).all() and not torch.isfinite(h[1:]).any()
 
 
-@pytest.mark.parametrize("C,every", [(8, 97), (128, 384), (128, 161), (33, 1531)])
+@pytest.mark.parametrize("C,every", [(8, 97), (128, 384), (128, 161), (33, 1531), (400, 193),
+                                     (400, 320), (1100, 161), (155, 700)])
 def test_many_sequences_on_few_channels(C, every):
     """Starts in every place of a tile and of a group of tiles, far more tiles than
     run at once."""
-    T = 120_000
+    T = 120_000 if C < 200 else 30_000
     lens = [every] * (T // every) + [T % every]
     x, g, init, _, _ = make(17, lens, 1, C, "f32", -3.0)
     X, G, I = cuda(x, g, init)
