@@ -149,6 +149,20 @@ def test_forward_and_backward_match_the_recurrence(lens, H, d, dtype):
     check_backward(x, g, init, dout, dfin, lens, again, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,d", [(1, 2052), (32, 64), (9, 128), (1, 301), (3, 128)])
+def test_rows_of_every_length(H, d, dtype):
+    """Tiles in groups of three and without groups, the backward pass's long rows."""
+    lens = [110, 133, 162, 0, 26, 343]
+    x, g, init, dout, dfin = make(d, lens, H, d, dtype)
+    X, G, I, D, F = cuda(x, g, init, dout, dfin)
+    cu = offsets(lens)
+    h, final, entry = kda.linear_scan(X, G, I, cu_seqlens=cu, output_entry_states=True)
+    check_forward(x, g, init, lens, h, final, dtype)
+    got = kda.linear_scan_bwd(X, G, D, I, F, cu_seqlens=cu, entry_states=entry)
+    check_backward(x, g, init, dout, dfin, lens, got, dtype)
+
+
 @pytest.mark.parametrize("gate", ["zero", "strong", "growth", -4.0])
 def test_gates_of_every_size(gate):
     lens = [700, 1, 500]
