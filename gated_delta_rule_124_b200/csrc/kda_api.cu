@@ -1008,6 +1008,16 @@ kda_status_t kda_fp8_matmul(const void* a8, const float* a_scale, const void* b8
                                             out_dtype, out, static_cast<cudaStream_t>(stream)));
 }
 
+kda_status_t kda_test_fp8_matmul_plan(int M, int N, int K, int b_block_rows, int sms,
+                                      int* tile_rows, int* split) {
+    if (M < 1 || N < 1 || K < 1 || M > kMaxFp8Dim || N > kMaxFp8Dim || K > kMaxFp8Dim ||
+        sms < 1 || sms > 1024 || !tile_rows || !split)
+        return KDA_ERR_INVALID_ARG;
+    if (b_block_rows != 1 && b_block_rows != 128) return KDA_ERR_UNSUPPORTED;
+    kda::fp8_matmul_plan(M, N, K, b_block_rows == 1, sms, tile_rows, split);
+    return KDA_OK;
+}
+
 // ----------------------------------------------------------------- status
 
 kda_status_t kda_get_device_status(void* workspace, void* stream) {

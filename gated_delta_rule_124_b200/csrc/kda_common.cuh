@@ -315,6 +315,7 @@ inline int blocks128(int n) { return (n + 127) / 128; }
 cudaError_t launch_quantize(const void* x, int rows, int cols, kda_dtype_t dt, bool row_blocks,
                             bool transpose, void* y8, float* scale, cudaStream_t st);
 bool fp8_matmul_available();
+void fp8_matmul_plan(int M, int N, int K, bool b_rows, int sms, int* tile_rows, int* split);
 cudaError_t launch_fp8_small(const void* a8, const float* a_scale, const void* b8,
                              const float* b_scale, int M, int N, int K, bool b_rows,
                              kda_dtype_t out_dt, void* out, cudaStream_t st);

@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (a.split > 1) {
+            group_sync(1, kThreads);
             cluster_sync();
             cluster_sync();
         }
@@ -579,8 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // NaN instead of a sum that lacks blocks
             if (!ok) sums.fill(0x7FFFFFFF7FFFFFFFull);
             if (a.split > 1) {
-                // [row][column], where the stages were: every load of this CTA
-                // has been consumed
+                // [row][column], where the stages were, once every warp of the CTA
+                // is done with them: with 256 rows of B a group's sums wait for
+                // their own half's products only, and those of the other half may
+                // be blocks behind, reading the same stages
+                group_sync(1, kThreads);
                 if (m < a.M)
                     sums.partial(reinterpret_cast<float*>(stages) + quarter * 32 * P::kPartPitch +
                                      wg * NC,
@@ -921,6 +925,28 @@ cudaError_t run_few(const void* a8, const void* b8, const MatmulArgs& a, int K, 
                   tmx, a);
 }
 
+// Which kernel a product takes.  bn: rows of B per tile of the first one; kFewRowsPlan:
+// changed places; kNoStagesPlan: kda_fp8_small.cu.
+constexpr int kFewRowsPlan = 0, kNoStagesPlan = -1;
+void plan(int M, int N, int K, bool b_rows, int sms, int* bn, int* split) {
+    // few rows: the kernel without stages while it takes a round or two (of 4096
+    // columns by 32 rows of B an SM), then the one of changed places (us, 8 and 16
+    // rows of A: 4096 x 4096 6.5 and 9.7 against 9.0 and 9.3, 4096 x 2048 4.7 and 6.5
+    // against 8.0, 8192 x 4096 11.0 and 17.5 against 11.8, 12288 x 4096 15.4 and 24.9
+    // against 14.4)
+    *split = 1;
+    const long long rounds =
+        ((long long)N + 32 * sms - 1) / (32 * sms) * (((long long)K + 4095) / 4096);
+    if (M <= 8 ? rounds <= 2 : M <= kFewRows && rounds <= 1) {
+        *bn = kNoStagesPlan;
+    } else if (M <= kFewRows) {
+        *bn = kFewRowsPlan;
+        *split = few_split(blocks128(N), blocks128(K), sms);
+    } else {
+        choose(M, N, blocks128(K), b_rows, sms, bn, split);
+    }
+}
+
 cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale, const void* b8,
                         const float* b_scale, int M, int N, int K, bool b_rows,
                         kda_dtype_t out_dt, void* out, int sms, cudaStream_t st) {
@@ -934,14 +960,13 @@ cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale,
     a.NB = b_rows ? N : blocks128(N);
     a.out_bf16 = out_dt == KDA_DTYPE_BF16;
     a.out_wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
-    if (bn == 0) {  // few rows
+    a.split = split;
+    if (bn == kFewRowsPlan) {
         a.tiles = blocks128(N);
-        a.split = few_split(a.tiles, a.KB, sms);
         if ((long long)a.tiles * a.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
         return b_rows ? run_few<true>(a8, b8, a, K, st) : run_few<false>(a8, b8, a, K, st);
     }
     a.ntm = static_cast<int>(((long long)M + kRowsA - 1) / kRowsA);
-    a.split = split;
     const long long tiles = (long long)a.ntm * (((long long)N + bn - 1) / bn);
     if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<int>(tiles);
@@ -954,6 +979,10 @@ cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale,
 
 bool fp8_matmul_available() { return encode_fn() != nullptr; }
 
+void fp8_matmul_plan(int M, int N, int K, bool b_rows, int sms, int* tile_rows, int* split) {
+    plan(M, N, K, b_rows, sms, tile_rows, split);
+}
+
 cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
                               const float* b_scale, int M, int N, int K, bool b_rows,
                               kda_dtype_t out_dt, void* out, cudaStream_t st) {
@@ -962,16 +991,10 @@ cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* 
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // few rows: the kernel without stages while it takes a round or two (of 4096
-    // columns by 32 rows of B an SM), then the one of changed places (us, 8 and 16
-    // rows of A: 4096 x 4096 6.5 and 9.7 against 9.0 and 9.3, 4096 x 2048 4.7 and 6.5
-    // against 8.0, 8192 x 4096 11.0 and 17.5 against 11.8, 12288 x 4096 15.4 and 24.9
-    // against 14.4)
-    const long long rounds = ((long long)N + 32 * sms - 1) / (32 * sms) * ((K + 4095) / 4096);
-    if (M <= 8 ? rounds <= 2 : M <= kFewRows && rounds <= 1)
+    int bn = 0, split = 1;
+    plan(M, N, K, b_rows, sms, &bn, &split);
+    if (bn == kNoStagesPlan)
         return launch_fp8_small(a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, st);
-    int bn = 0, split = 1;  // bn 0: changed places
-    if (M > kFewRows) choose(M, N, blocks128(K), b_rows, sms, &bn, &split);
     return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, sms, st);
 }
 

@@ -52,7 +52,7 @@ EXPORTS = (
     "kda_linear_scan_bwd_workspace_size", "kda_linear_scan_fwd", "kda_linear_scan_bwd",
     "kda_linear_scan_step", "kda_fp8_pitch", "kda_add_rms_norm",
     "kda_add_rms_norm_bwd_workspace_size", "kda_add_rms_norm_bwd", "kda_quantize_fp8",
-    "kda_fp8_matmul",
+    "kda_fp8_matmul", "kda_test_fp8_matmul_plan",
 )
 
 
@@ -114,6 +114,7 @@ _SIGS = {
     "kda_add_rms_norm_bwd": ([_vp] * 4 + [_i] * 3 + [ctypes.c_float] + [_vp] * 3 + [_sz, _vp], _i),
     "kda_quantize_fp8": ([_vp] + [_i] * 5 + [_vp] * 3, _i),
     "kda_fp8_matmul": ([_vp] * 4 + [_i] * 5 + [_vp] * 2, _i),
+    "kda_test_fp8_matmul_plan": ([_i] * 5 + [_vp] * 2, _i),
 }
 
 # Size of the library's built-in scratch used by kda_chunk_fwd_noalloc.
@@ -678,6 +679,15 @@ def kda_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, o
                                       (b_scale, _F32), (out, (_TORCH_OF[code],)))
     return _enqueue("kda_fp8_matmul", dev, stream, check, pa, ps, pb, pt, M, N, K, b_block_rows,
                     code, po)
+
+
+def kda_test_fp8_matmul_plan(M, N, K, b_block_rows, sms=148) -> tuple:
+    """(tile_rows, split) of the kernel that kda_fp8_matmul takes.  Testing only."""
+    rows, split = ctypes.c_int(), ctypes.c_int()
+    st = load().kda_test_fp8_matmul_plan(M, N, K, b_block_rows, sms, ctypes.byref(rows),
+                                         ctypes.byref(split))
+    _ret(st, "kda_test_fp8_matmul_plan", True)
+    return rows.value, split.value
 
 
 def kda_chunk_fwd_noalloc(q, k, v, g, beta, initial_state, cu_seqlens, B, T, num_seqs, H, dk,

@@ -687,6 +687,16 @@ kda_status_t kda_test_overlap_flag_timeout(const void* q, const void* k, const v
                                            int withheld_chunk, int withheld_head,
                                            unsigned long long flag_wait_ns, void* stream);
 
+/* kda_test_fp8_matmul_plan: the kernel that kda_fp8_matmul takes for a product of
+ * these sizes on a device of `sms` SMs (no device is needed).  *tile_rows: rows of b
+ * per output tile of 128 rows of a (256 or 128), 0 for the kernel of few rows of a
+ * whose tile is 128 rows of b, -1 for the one without stages; *split: the CTAs that
+ * share a tile's blocks of K.  It lets the tests name the variant that each of their
+ * sizes reaches.
+ */
+kda_status_t kda_test_fp8_matmul_plan(int M, int N, int K, int b_block_rows, int sms,
+                                      int* tile_rows, int* split);
+
 /* ------------------------------------------------------------------ status
  * Synchronises `stream`, then reads the device status word kept at the start
  * of `workspace`.  Every prefill call (kda_chunk_fwd and the step calls)

@@ -1,0 +1,116 @@
+"""The variants of the 8-bit product, each at sizes that reach it: which one a size
+takes is asserted on the host, so that the GPU tests below cannot lose their variant.
+
+Error bound as for the other products: e4m3 products are exact, at most 128
+additions inside a block, K / 128 blocks, 8 parts and three roundings of scales,
+each at most 2 u (u = 2^-24; the tensor cores may cut off instead of rounding) of
+the sum of magnitudes; then the output's rounding (bf16 2^-8, fp32 2^-24)."""
+import pytest
+import torch
+
+import gated_delta_rule_124_b200 as kda
+from gated_delta_rule_124_b200 import build as kbuild
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": U}
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+# (M, N, K, b_block_rows): rows of b per tile, CTAs per tile.  Down projections and
+# weight gradients over long batches among them, and sizes that end inside a tile, a
+# block of 128 and a 16-byte piece.
+SPLIT_256 = {
+    (512, 4096, 8192, 128): 2, (512, 4096, 8192, 1): 2, (500, 4001, 8190, 128): 2,
+    (500, 4001, 8190, 1): 2, (256, 5120, 6144, 128): 3, (250, 5001, 6100, 1): 3,
+    (250, 5001, 6100, 128): 3, (1024, 1024, 16384, 1): 4, (1000, 1010, 16401, 128): 4,
+    (64, 6101, 8200, 128): 4, (64, 6101, 8200, 1): 4, (128, 2048, 14336, 128): 8,
+    (128, 2048, 14336, 1): 8, (70, 2001, 14401, 128): 8, (17, 2001, 14301, 1): 8,
+}
+WHOLE_256 = {(4090, 4090, 4101, 1): 1, (3900, 4001, 1000, 1): 1, (2100, 4090, 300, 1): 1,
+             (4090, 4090, 4101, 128): 1, (2100, 4090, 300, 128): 1}
+OTHERS = {  # the variants of other tests: (rows of b per tile, CTAs per tile)
+    (20, 1000, 4100, 128): (128, 8), (130, 2500, 4096, 128): (128, 3),
+    (200, 4096, 3000, 1): (128, 2), (513, 1100, 300, 1): (128, 1),
+    (16, 5000, 1100, 128): (0, 1), (9, 300, 9000, 128): (0, 8), (13, 4901, 3100, 1): (0, 4),
+    (16, 9601, 8200, 1): (0, 2), (8, 9500, 4100, 128): (0, 1), (16, 256, 1024, 128): (-1, 1),
+    (2, 4096, 2048, 1): (-1, 1),
+}
+
+
+def test_sizes_take_the_variant_that_they_test():
+    kbuild.build()
+    for sizes, split in {**SPLIT_256, **WHOLE_256}.items():
+        assert kda.kda_test_fp8_matmul_plan(*sizes) == (256, split), sizes
+    for sizes, want in OTHERS.items():
+        assert kda.kda_test_fp8_matmul_plan(*sizes) == want, sizes
+
+
+def test_plan_refusals():
+    kbuild.build()
+    for sizes in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 1, 0, 1), (1, 1, 1, 1, 0)):
+        with pytest.raises(RuntimeError):
+            kda.kda_test_fp8_matmul_plan(*sizes)
+    with pytest.raises(RuntimeError):
+        kda.kda_test_fp8_matmul_plan(1, 1, 1, 64)
+    # the largest sizes that the library takes, on devices of other sizes
+    for sms in (1, 2, 148, 160, 1024):
+        for M in (1, 16, 17, 0x7fffff00):
+            rows, split = kda.kda_test_fp8_matmul_plan(M, 0x7fffff00, 0x7fffff00, 1, sms)
+            assert rows in (-1, 0, 128, 256) and split in (1, 2, 3, 4, 8)
+
+
+def operands(seed, M, N, K, block):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    a = torch.randn(M, K, generator=gen, device="cuda")
+    a *= torch.exp(torch.randn(M, 1, generator=gen, device="cuda"))
+    b = torch.randn(N, K, generator=gen, device="cuda")
+    return (*kda.quantize_fp8(a), *kda.quantize_fp8(b, block_rows=block))
+
+
+def values(y8, scale, K, block):
+    """The matrix that the codes stand for, in 64 bits."""
+    s = scale.double().t().repeat_interleave(block, 0)[:y8.shape[0]]
+    return y8[:, :K].double() * s.repeat_interleave(128, 1)[:, :K]
+
+
+def check(out, a8, sa, b8, sb, K, block, out_dtype):
+    a, b = values(a8, sa, K, 1), values(b8, sb, K, block)
+    want, mag = a @ b.t(), a.abs() @ b.abs().t()
+    tol = 2 * (128 + K / 128 + 8 + 3) * U * mag + HALF[out_dtype] * want.abs()
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), (err / mag.clamp_min(1e-30)).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K,block", [*SPLIT_256, *WHOLE_256])
+def test_wide_tiles(M, N, K, block, out_dtype):
+    """Tiles of 256 rows of b, whole and split two, three, four and eight ways, with
+    the same bits every time."""
+    a8, sa, b8, sb = operands(M + N + K, M, N, K, block)
+    out = torch.full((M + 2, N), float("nan"), dtype=DT[out_dtype], device="cuda")
+    kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out=out[:M])
+    check(out[:M], a8, sa, b8, sb, K, block, out_dtype)
+    assert torch.isnan(out[M:]).all()     # rows behind the last one stay as they were
+    again = torch.empty_like(out[:M])
+    for _ in range(20):
+        again.zero_()
+        kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out=again)
+        assert torch.equal(again, out[:M])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block", [128, 1])
+def test_wide_split_tiles_beside_other_work(block):
+    """Two products at once, on two streams, each with the bits it has alone."""
+    first, second = operands(1, 512, 4096, 8192, block), operands(2, 128, 2048, 14336, block)
+    alone = [kda.fp8_matmul(*args, b_block_rows=block, out_dtype=torch.float32)
+             for args in (first, second)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(10):
+        for stream, args in zip(streams, (first, second)):
+            with torch.cuda.stream(stream):
+                outs.append(kda.fp8_matmul(*args, b_block_rows=block, out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, alone[i % 2])
