@@ -32,7 +32,8 @@
 // and the products alone 512.  Giving each half of a last, part-filled round of
 // tiles to a CTA of its own gained nothing: a half takes a block as long.
 //
-// Every wait is bounded; a tile whose waits gave up is written as NaN.
+// Every wait is bounded; a tile whose waits gave up, and every later one of its CTA,
+// is written as NaN.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -76,15 +77,20 @@ struct MatmulArgs {
     int M, N, KB, NB; // NB: columns of sb
     int out_bf16, out_wide;  // wide: out starts on 32 bytes
     int ntm, tiles, split;
+    Fp8Timeout timeout;
+    // The block that this CTA's loads leave out (-1: none; tests of the waits).
+    __device__ __forceinline__ int withheld() const {
+        return static_cast<int>(blockIdx.x) == timeout.cta ? timeout.block : -1;
+    }
 };
 
 // Bounded wait on a phase parity (some seconds at most).  A test before the loop
 // and a plain loop of tests: the waits of the threads that issue the products
 // are mostly for phases that are complete, and with only a loop (or one with a
 // clock and a sleep in it) such a wait took 140 to 250 cycles more.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const MatmulArgs& a) {
     if (mbar_test_wait(bar, parity)) return true;
-    for (int i = 0; i < (1 << 26); ++i)
+    for (int i = 0; i < a.timeout.tests; ++i)
         if (mbar_test_wait(bar, parity)) return true;
     return false;
 }
@@ -427,14 +433,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             if (elect_one()) {
                 int it = 0;
+                const int withheld = a.withheld();
                 for (int tile = first; tile < a.tiles && !*fail; tile += step) {
                     const int m0 = tile % a.ntm * kRowsA, n0 = tile / a.ntm * BN;
                     for (int kb = kb0; kb < kb1; ++kb, ++it) {
                         const int s = it % ST;
-                        if (!wait(&empty[s], ((it / ST) & 1) ^ 1)) {
+                        if (!wait(&empty[s], ((it / ST) & 1) ^ 1, a)) {
                             *fail = 1;
                             break;
                         }
+                        if (it == withheld) continue;
                         uint8_t* st = stages + s * P::kStage;
                         mbar_arrive_expect_tx(&full[s], P::kStage);
                         tma_load_2d(st, &tma, &full[s], kb * 128, m0);
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // loads in flight land before the CTA may end (a no-op unless
                 // a wait gave up: the products have waited for every load)
                 for (int s = 0; s < ST && s < it; ++s)
-                    wait(&full[s], ((it - 1 - s) / ST) & 1);
+                    wait(&full[s], ((it - 1 - s) / ST) & 1, a);
             }
         } else if (warp < 3) {
             if (elect_one()) {
@@ -456,11 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int h = HV == 2 ? warp - 1 : 0, u = it * HV + h;
                         if (HV == 1 && (u & 1) != warp - 1) continue;
                         const int s = it % ST, b = u % NB;
-                        if (!wait(&full[s], (it / ST) & 1)) {
+                        if (!wait(&full[s], (it / ST) & 1, a)) {
                             *fail = 1;
                             break;
                         }
-                        if (!wait(&tempty[b], ((u / NB) & 1) ^ 1)) {
+                        if (!wait(&tempty[b], ((u / NB) & 1) ^ 1, a)) {
                             *fail = 1;
                             break;
                         }
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // no product is in flight when the tensor memory goes back
-                if (last >= 0) wait(&tfull[last % NB], (last / NB) & 1);
+                if (last >= 0) wait(&tfull[last % NB], (last / NB) & 1, a);
             }
         } else {
             // scales: the values of the next blocks (across tiles) are requested
@@ -523,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < GROUP; ++u) {
                     if (u >= count) break;
                     const int s = it % ST;
-                    if (!wait(&sempty[s], ((it / ST) & 1) ^ 1)) {
+                    if (!wait(&sempty[s], ((it / ST) & 1) ^ 1, a)) {
                         *fail = 1;
                         break;
                     }
@@ -553,15 +561,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t tq = tmem + (static_cast<uint32_t>(quarter) << 21) + (HV == 1 ? wg * NC : 0);
         int it = 0;
+        bool ok = true;
         for (int tile = first; tile < a.tiles; tile += step) {
             const int m = tile % a.ntm * kRowsA + quarter * 32;
             const int n = tile / a.ntm * BN + wg * NC;
             typename std::conditional<kRowScales, FragSums<NC>, RowSums<NC>>::type sums;
             sums.fill(0ull);
-            bool ok = true;
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                 const int u = HV == 1 ? it : it * HV + wg, b = u % NB, s = it % ST;
-                ok = __all_sync(0xffffffffu, wait(&tfull[b], (u / NB) & 1));
+                ok = __all_sync(0xffffffffu, wait(&tfull[b], (u / NB) & 1, a));
                 if (!ok) {
                     *fail = 1;
                     break;
@@ -592,7 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             sums.store(a, m, n, lane);
-            if (!ok) break;
         }
         if (a.split > 1) {
             __syncwarp();
@@ -680,12 +687,14 @@ __global__ void __launch_bounds__(kFewThreads)
     if (warp == 0) {
         if (elect_one()) {
             int it = 0;
+            const int withheld = a.withheld();
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST;
-                if (*fail || !wait(&empty[s], ((it / ST) & 1) ^ 1)) {
+                if (*fail || !wait(&empty[s], ((it / ST) & 1) ^ 1, a)) {
                     *fail = 1;
                     break;
                 }
+                if (it == withheld) continue;
                 uint8_t* st = stages + s * kFewStage;
                 mbar_arrive_expect_tx(&full[s], kFewStage);
                 tma_load_2d(st, &tmw, &full[s], kb * 128, n0);
@@ -693,7 +702,7 @@ __global__ void __launch_bounds__(kFewThreads)
             }
             // loads in flight land before the stages are written again (a no-op
             // unless a wait gave up: the products have waited for every load)
-            for (int s = 0; s < ST && s < it; ++s) wait(&full[s], ((it - 1 - s) / ST) & 1);
+            for (int s = 0; s < ST && s < it; ++s) wait(&full[s], ((it - 1 - s) / ST) & 1, a);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -701,7 +710,7 @@ __global__ void __launch_bounds__(kFewThreads)
             int it = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST, b = it % NB;
-                if (!wait(&full[s], (it / ST) & 1) || !wait(&tempty[b], ((it / NB) & 1) ^ 1)) {
+                if (!wait(&full[s], (it / ST) & 1, a) || !wait(&tempty[b], ((it / NB) & 1) ^ 1, a)) {
                     *fail = 1;
                     break;
                 }
@@ -715,7 +724,7 @@ __global__ void __launch_bounds__(kFewThreads)
                 mma_commit(&empty[s]);
             }
             // no product is in flight when the tensor memory goes back
-            if (it > 0) wait(&tfull[(it - 1) % NB], ((it - 1) / NB) & 1);
+            if (it > 0) wait(&tfull[(it - 1) % NB], ((it - 1) / NB) & 1, a);
         }
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -743,7 +752,7 @@ __global__ void __launch_bounds__(kFewThreads)
             for (int u = 0; u < NB; ++u) {  // block u of these is in buffer u
                 const int kb = base + u, it = kb - kb0;
                 if (kb >= kb1 || !ok) break;
-                ok = __all_sync(0xffffffffu, wait(&tfull[u], (it / NB) & 1));
+                ok = __all_sync(0xffffffffu, wait(&tfull[u], (it / NB) & 1, a));
                 if (!ok) {
                     *fail = 1;
                     break;
@@ -779,6 +788,8 @@ __global__ void __launch_bounds__(kFewThreads)
                 }
             }
         } else {
+            // (after the loads and products of a CTA whose waits gave up, too)
+            group_sync(1, kFewThreads);
 #pragma unroll
             for (int m = 0; m < MP; ++m)
                 if (m < a.M) part[m * kRowsA + row] = acc[m];
@@ -786,6 +797,7 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     __syncwarp();
     if (a.split > 1) {
+        if (warp < 2) group_sync(1, kFewThreads);
         cluster_sync();
         // this CTA's share of the tile, neighbouring rows of B in neighbouring lanes
         const int all = a.M * (kRowsA / 4);
@@ -949,8 +961,10 @@ void plan(int M, int N, int K, bool b_rows, int sms, int* bn, int* split) {
 
 cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale, const void* b8,
                         const float* b_scale, int M, int N, int K, bool b_rows,
-                        kda_dtype_t out_dt, void* out, int sms, cudaStream_t st) {
+                        kda_dtype_t out_dt, void* out, const Fp8Timeout& timeout, int sms,
+                        cudaStream_t st) {
     MatmulArgs a{};
+    a.timeout = timeout;
     a.sa = a_scale;
     a.sb = b_scale;
     a.out = out;
@@ -985,7 +999,8 @@ void fp8_matmul_plan(int M, int N, int K, bool b_rows, int sms, int* tile_rows, 
 
 cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
                               const float* b_scale, int M, int N, int K, bool b_rows,
-                              kda_dtype_t out_dt, void* out, cudaStream_t st) {
+                              kda_dtype_t out_dt, void* out, cudaStream_t st,
+                              const Fp8Timeout& timeout) {
     if (M == 0) return cudaSuccess;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -993,9 +1008,11 @@ cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* 
     if (e != cudaSuccess) return e;
     int bn = 0, split = 1;
     plan(M, N, K, b_rows, sms, &bn, &split);
+    if (bn == kNoStagesPlan && timeout.cta >= 0) return cudaErrorNotSupported;  // (no waits)
     if (bn == kNoStagesPlan)
         return launch_fp8_small(a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, st);
-    return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, sms, st);
+    return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, timeout, sms,
+                       st);
 }
 
 }  // namespace kda

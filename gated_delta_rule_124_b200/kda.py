@@ -52,7 +52,7 @@ EXPORTS = (
     "kda_linear_scan_bwd_workspace_size", "kda_linear_scan_fwd", "kda_linear_scan_bwd",
     "kda_linear_scan_step", "kda_fp8_pitch", "kda_add_rms_norm",
     "kda_add_rms_norm_bwd_workspace_size", "kda_add_rms_norm_bwd", "kda_quantize_fp8",
-    "kda_fp8_matmul", "kda_test_fp8_matmul_plan",
+    "kda_fp8_matmul", "kda_test_fp8_matmul_timeout", "kda_test_fp8_matmul_plan",
 )
 
 
@@ -114,6 +114,7 @@ _SIGS = {
     "kda_add_rms_norm_bwd": ([_vp] * 4 + [_i] * 3 + [ctypes.c_float] + [_vp] * 3 + [_sz, _vp], _i),
     "kda_quantize_fp8": ([_vp] + [_i] * 5 + [_vp] * 3, _i),
     "kda_fp8_matmul": ([_vp] * 4 + [_i] * 5 + [_vp] * 2, _i),
+    "kda_test_fp8_matmul_timeout": ([_vp] * 4 + [_i] * 5 + [_vp] + [_i] * 3 + [_vp], _i),
     "kda_test_fp8_matmul_plan": ([_i] * 5 + [_vp] * 2, _i),
 }
 
@@ -679,6 +680,18 @@ def kda_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, o
                                       (b_scale, _F32), (out, (_TORCH_OF[code],)))
     return _enqueue("kda_fp8_matmul", dev, stream, check, pa, ps, pb, pt, M, N, K, b_block_rows,
                     code, po)
+
+
+def kda_test_fp8_matmul_timeout(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, out,
+                                withheld_cta, withheld_block, wait_tests, stream=None,
+                                check=True) -> int:
+    """The product with one block of one CTA never loaded and the waits bounded by
+    wait_tests: exercises the bounded-wait error path (NaN).  Testing only."""
+    code = dtype_code(out_dtype)
+    (pa, ps, pb, pt, po), dev = _args("kda_test_fp8_matmul_timeout", (a8, _FP8), (a_scale, _F32),
+                                      (b8, _FP8), (b_scale, _F32), (out, (_TORCH_OF[code],)))
+    return _enqueue("kda_test_fp8_matmul_timeout", dev, stream, check, pa, ps, pb, pt, M, N, K,
+                    b_block_rows, code, po, withheld_cta, withheld_block, wait_tests)
 
 
 def kda_test_fp8_matmul_plan(M, N, K, b_block_rows, sms=148) -> tuple:

@@ -605,6 +605,7 @@ kda_status_t kda_linear_scan_step(const void* x, const float* g, const float* st
  *   projection's input; with both operands transposed (K: tokens,
  *   b_block_rows 1) the gradient of its weight.  Any M >= 0, N >= 1, K >= 1.
  *   No workspace.  KDA_ERR_UNSUPPORTED without a driver that makes tensor maps.
+ *   Every wait of its kernels is bounded: a part of out whose waits gave up is NaN.
  */
 int kda_fp8_pitch(int K);
 
@@ -686,6 +687,21 @@ kda_status_t kda_test_overlap_flag_timeout(const void* q, const void* k, const v
                                            void* workspace, size_t workspace_bytes,
                                            int withheld_chunk, int withheld_head,
                                            unsigned long long flag_wait_ns, void* stream);
+
+/* kda_test_fp8_matmul_timeout: kda_fp8_matmul with block `withheld_block` (counted
+ * over the CTA's output tiles) of CTA `withheld_cta` never loaded, and every wait
+ * bounded by wait_tests (2^16 .. 2^26) looks at its barrier instead of 2^26.  The
+ * waits that need that block give up; the CTA waits for its own copies and products
+ * in flight and writes NaN for the tile that lacks the block and for its later
+ * tiles, every other tile as kda_fp8_matmul does.  A CTA or block that the call does
+ * not have is withheld from nothing.  KDA_ERR_CUDA where the call takes the kernel
+ * without waits (tile_rows -1, below).  Not a computation: only tests need it.
+ */
+kda_status_t kda_test_fp8_matmul_timeout(const void* a8, const float* a_scale, const void* b8,
+                                         const float* b_scale, int M, int N, int K,
+                                         int b_block_rows, kda_dtype_t out_dtype, void* out,
+                                         int withheld_cta, int withheld_block, int wait_tests,
+                                         void* stream);
 
 /* kda_test_fp8_matmul_plan: the kernel that kda_fp8_matmul takes for a product of
  * these sizes on a device of `sms` SMs (no device is needed).  *tile_rows: rows of b

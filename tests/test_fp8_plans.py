@@ -114,3 +114,51 @@ def test_wide_split_tiles_beside_other_work(block):
     torch.cuda.synchronize()
     for i, out in enumerate(outs):
         assert torch.equal(out, alone[i % 2])
+
+
+def test_timeout_hook_refusals():
+    kbuild.build()
+    fake = 1 << 20
+    ok = dict(a8=fake, a_scale=fake, b8=fake, b_scale=fake, M=20, N=64, K=64, b_block_rows=128,
+              out_dtype="bf16", out=fake, withheld_cta=0, withheld_block=0, wait_tests=1 << 16,
+              stream=0, check=False)
+    for change in (dict(withheld_cta=-1), dict(withheld_block=-1), dict(wait_tests=(1 << 16) - 1),
+                   dict(wait_tests=(1 << 26) + 1), dict(out=None), dict(K=0)):
+        assert kda.kda_test_fp8_matmul_timeout(**{**ok, **change}) == kda.KDA_ERR_INVALID_ARG, change
+    assert kda.kda_test_fp8_matmul_timeout(**{**ok, "M": 0}) == kda.KDA_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,block,cta,withheld", [
+    (2100, 4090, 300, 1, 3, 1), (2100, 4090, 300, 128, 3, 4),   # both tiles of a CTA, the second
+    (5120, 1024, 130, 1, 4, 3), (9500, 520, 700, 128, 5, 8),
+    (20, 1000, 4100, 128, 9, 1), (250, 5001, 6100, 1, 7, 3), (64, 6101, 8200, 128, 2, 0),
+    (16, 5000, 1100, 1, 6, 8), (13, 4901, 3100, 128, 5, 2), (9, 300, 9000, 128, 17, 8)])
+def test_tiles_whose_waits_give_up_are_nan(M, N, K, block, cta, withheld):
+    """One block of one CTA is never loaded: the tile that lacks it and the CTA's later
+    ones are NaN throughout, everything else has the bits of the ordinary call, and
+    the next call is right again."""
+    a8, sa, b8, sb = operands(M + K, M, N, K, block)
+    want = kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out_dtype=torch.float32)
+    got = torch.zeros_like(want)
+    kda.kda_test_fp8_matmul_timeout(a8, sa, b8, sb, M, N, K, block, "f32", got, cta, withheld,
+                                    1 << 18)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows, split = kda.kda_test_fp8_matmul_plan(M, N, K, block, sms)
+    KB, ntm, bn = -(-K // 128), -(-M // 128), rows or 128
+    tiles = ntm * -(-N // bn)
+    lost = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    if split > 1 or rows == 0:
+        rank = cta % split
+        assert withheld < KB * (rank + 1) // split - KB * rank // split
+        mine = [cta // split]
+    else:
+        mine = list(range(cta, tiles, min(tiles, sms)))[withheld // KB:]
+    assert mine and mine[-1] < tiles
+    for t in mine:
+        m, n = t % ntm * 128, t // ntm * bn
+        lost[m:m + 128, n:n + bn] = True
+    assert torch.isnan(got[lost]).all() and torch.equal(got[~lost], want[~lost])
+    got.zero_()
+    kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out=got)
+    assert torch.equal(got, want)
