@@ -26,4 +26,5 @@ from .kda import (  # noqa: F401
     kda_add_rms_norm_bwd_workspace_size, add_rms_norm, add_rms_norm_bwd, AddRMSNorm,
     residual_rms_norm, kda_quantize_fp8, quantize_fp8, kda_fp8_matmul, fp8_matmul, Fp8Linear,
     fp8_linear, kda_test_fp8_matmul_plan, kda_test_fp8_matmul_timeout,
+    kda_test_linear_scan_timeout,
 )

@@ -925,6 +925,32 @@ kda_status_t kda_linear_scan_bwd(const void* x, const float* g, const float* ini
                                           static_cast<cudaStream_t>(stream)));
 }
 
+kda_status_t kda_test_linear_scan_timeout(const void* x, const float* g, const void* dout,
+                                          const float* entry_states, int T, int H, int d,
+                                          kda_dtype_t dtype, void* out, float* dg,
+                                          void* workspace, size_t workspace_bytes,
+                                          unsigned long long wait_ns, void* stream) {
+    if (wait_ns == 0 || wait_ns > 2000000000ull) return KDA_ERR_INVALID_ARG;
+    Prefill p;
+    const kda_status_t s =
+        dout ? check_scan(nullptr, 1, T, 1, H, d, dtype, workspace, workspace_bytes, true,
+                          {x, g, dout, out, dg}, {entry_states}, &p)
+             : check_scan(nullptr, 1, T, 1, H, d, dtype, workspace, workspace_bytes, false,
+                          {x, g, out}, {}, &p);
+    if (s != KDA_OK) return s;
+    if (p.total <= 256) return KDA_ERR_INVALID_ARG;  // one tile: nothing waits
+    kda::ScanTimeout timeout;
+    timeout.wait_ns = wait_ns;
+    timeout.withhold = true;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!dout)
+        return from_cuda(kda::launch_scan_fwd(x, g, nullptr, nullptr, T, p.total, p.N, H * d, dtype,
+                                              out, nullptr, nullptr, workspace, st, timeout));
+    return from_cuda(kda::launch_scan_bwd(x, g, nullptr, dout, nullptr, entry_states, nullptr, T,
+                                          p.total, p.N, H * d, dtype, out, dg, nullptr, workspace,
+                                          st, timeout));
+}
+
 kda_status_t kda_linear_scan_step(const void* x, const float* g, const float* state_in,
                                   float* state_out, void* h, int N, int H, int d,
                                   kda_dtype_t dtype, void* stream) {

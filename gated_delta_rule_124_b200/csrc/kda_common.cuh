@@ -290,13 +290,21 @@ inline size_t scan_tiles(int total) {
     return total > 0 ? ((size_t)total + kScanRows - 1) / kScanRows : 1;
 }
 size_t scan_workspace_bytes(int total, int C, bool backward);
+// The limit of a tile's wait for the tiles before it.  withhold (a test of that limit):
+// the first tile of the call's first pass is never run.
+struct ScanTimeout {
+    unsigned long long wait_ns = 2000000000ull;
+    bool withhold = false;
+};
 cudaError_t launch_scan_fwd(const void* x, const float* g, const float* h0, const int32_t* cu,
                             int T, int total, int N, int C, kda_dtype_t dt, void* h,
-                            float* final_state, float* entry, void* workspace, cudaStream_t st);
+                            float* final_state, float* entry, void* workspace, cudaStream_t st,
+                            const ScanTimeout& timeout = ScanTimeout());
 cudaError_t launch_scan_bwd(const void* x, const float* g, const float* h0, const void* dout,
                             const float* dfinal, const float* entry, const int32_t* cu, int T,
                             int total, int N, int C, kda_dtype_t dt, void* dx, float* dg,
-                            float* dh0, void* workspace, cudaStream_t st);
+                            float* dh0, void* workspace, cudaStream_t st,
+                            const ScanTimeout& timeout = ScanTimeout());
 cudaError_t launch_scan_step(const void* x, const float* g, const float* state_in,
                              float* state_out, long long n, kda_dtype_t dt, void* h,
                              cudaStream_t st);

@@ -65,7 +65,6 @@ constexpr int kThreads = 32 * kWarps;
 // multiple of the kScanRows between entry states.
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;   // NaNs: no sum of logarithms is one
 constexpr uint32_t kExit = 0xFFFFFFFEu;
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kDepth = 64;             // groups' maps a look-back passes at most
 
 struct ScanArgs {
@@ -86,6 +85,9 @@ struct ScanArgs {
     uint32_t* ticket;       // starts at 0xFFFFFFFF; NULL: one tile per channel block
     uint64_t* words;        // [tiles, C] maps, then [groups, C]
     int tiles, ctiles;      // of the launched kernel's size
+    int keep_status;        // a pass of the same call has set the status word
+    int first_task;         // the tasks before it are never run (0; tests of the waits)
+    unsigned long long wait_ns;  // limit of a wait for a word
 };
 
 // How x, g and dout are loaded (every element once): past L1, or with L1's and
@@ -204,7 +206,7 @@ __device__ __forceinline__ uint64_t read_word(const uint64_t* w) {
 
 // A word once it is there (for `exit_only`: once it is an exit state).
 __device__ __forceinline__ uint64_t await_word(const uint64_t* w, uint64_t v, bool exit_only,
-                                               uint32_t* status) {
+                                               const ScanArgs& a) {
     const auto ready = [&] {
         const uint32_t lo = static_cast<uint32_t>(v);
         return exit_only ? lo == kExit : lo != kNotYet;
@@ -214,8 +216,8 @@ __device__ __forceinline__ uint64_t await_word(const uint64_t* w, uint64_t v, bo
     do {
         v = read_word(w);
         if (ready()) return v;
-    } while (sm100::global_timer_ns() - t0 <= kWaitNs);
-    atomicOr(status, STATUS_TIMEOUT);
+    } while (sm100::global_timer_ns() - t0 <= a.wait_ns);
+    atomicOr(a.status, STATUS_TIMEOUT);
     return kExit;  // (a state of 0; the outputs of the call are unspecified)
 }
 __device__ __forceinline__ float map_G(uint64_t v) {
@@ -229,7 +231,7 @@ __device__ __forceinline__ float map_b(uint64_t v) {
 // published its own (group 0 always does), through the maps of the groups between
 // in their order.  Maps found on the way back are kept (in local memory); behind
 // kDepth of them only an exit state will do.
-__device__ float group_exit(const uint64_t* groups, size_t C, int g, uint32_t* status) {
+__device__ float group_exit(const uint64_t* groups, size_t C, int g, const ScanArgs& a) {
     uint64_t kept[kDepth];
     int n = 0;
     const uint64_t* at = groups + (size_t)g * C;
@@ -238,7 +240,7 @@ __device__ float group_exit(const uint64_t* groups, size_t C, int g, uint32_t* s
     for (; g >= 0; --g, at -= C) {
         uint64_t v = next;
         if (g > 0) next = read_word(at - C);
-        v = await_word(at, v, n == kDepth || g == 0, status);
+        v = await_word(at, v, n == kDepth || g == 0, a);
         if (static_cast<uint32_t>(v) == kExit) {
             h = map_b(v);
             break;
@@ -276,7 +278,7 @@ __device__ float pass_tile(const ScanArgs& a, int ch, int pos, float G, float b,
         if (G != -INFINITY) {  // (a map that forgets needs none of the others)
 #pragma unroll
             for (int k = 0; k < kTiles - 1; ++k) {
-                v[k] = await_word(own + (size_t)k * C, v[k], false, a.status);
+                v[k] = await_word(own + (size_t)k * C, v[k], false, a);
                 bg = applied(half_gate(map_G(v[k])), map_b(v[k]), bg);
                 Gg += map_G(v[k]);
             }
@@ -287,13 +289,13 @@ __device__ float pass_tile(const ScanArgs& a, int ch, int pos, float G, float b,
         publish(groups + (size_t)g * C, Gg, bg, known);
     }
     float h = 0.f;
-    if (g > 0 && (needed || !known)) h = group_exit(groups, C, g - 1, a.status);
+    if (g > 0 && (needed || !known)) h = group_exit(groups, C, g - 1, a);
     if (!known) publish(groups + (size_t)g * C, 0.f, applied(half_gate(Gg), bg, h), true);
     if (!needed) return 0.f;
 #pragma unroll
     for (int k = 0; k < kTiles - 1; ++k) {
         if (k >= in) break;
-        v[k] = await_word(own + (size_t)k * C, v[k], false, a.status);
+        v[k] = await_word(own + (size_t)k * C, v[k], false, a);
         h = applied(half_gate(map_G(v[k])), map_b(v[k]), h);
     }
     return h;
@@ -352,7 +354,8 @@ __device__ __forceinline__ void find_bounds(const ScanArgs& a, int t0, Bounds<kR
 
 // Whether the offsets run from 0 to total without decreasing: the CTA of the
 // first tile and channels sets the status word (it starts before every CTA
-// that could report a timeout there, and such a report is seconds later).
+// that could report a timeout there, and such a report is seconds later); the
+// second pass of a call adds to what the first one left there.
 __device__ void report_status(const ScanArgs& a) {
     bool bad = false;
     if (a.cu) {
@@ -360,7 +363,9 @@ __device__ void report_status(const ScanArgs& a) {
         if (threadIdx.x == 0) bad |= a.cu[0] != 0 || a.cu[a.N] != a.total;
     }
     const int any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *a.status = any ? STATUS_BAD_SEQLENS : 0u;
+    if (threadIdx.x != 0) return;
+    if (!a.keep_status) *a.status = any ? STATUS_BAD_SEQLENS : 0u;
+    else if (any) atomicOr(a.status, STATUS_BAD_SEQLENS);
 }
 
 // States of empty sequences: nothing changes them (channels [c0, c0 + n)).
@@ -382,7 +387,7 @@ __device__ __forceinline__ int next_tile(const ScanArgs& a) {
     __shared__ uint32_t s_ticket;
     if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u) + 1u;
     __syncthreads();
-    return static_cast<int>(s_ticket);
+    return static_cast<int>(s_ticket) + a.first_task;
 }
 
 // A warp's rows of a tile in registers.  Lanes beyond the last channel load the
@@ -783,7 +788,8 @@ auto scan_kernel(bool backward) {
 }
 
 template <int VEC, int R, typename T>
-cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t st) {
+cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, bool withhold,
+                     cudaStream_t st) {
     static_assert(8 * R % kScanRows == 0, "a tile begins at an entry state");
     a.status = s.status;
     a.tiles = a.total > 0 ? static_cast<int>(((long long)a.total + 8 * R - 1) / (8 * R)) : 1;
@@ -791,6 +797,12 @@ cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t
     const long long grid = (long long)a.tiles * a.ctiles;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const int group = group_of(VEC, a.ctiles, backward);
+    if (withhold) {
+        if (a.tiles < 2) return cudaErrorInvalidConfiguration;  // (no tile waits)
+        a.first_task = a.ctiles;
+        const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(uint32_t), st);
+        if (e != cudaSuccess) return e;
+    }
     if (a.tiles > 1) {
         a.ticket = s.ticket;
         a.words = s.words;
@@ -804,23 +816,24 @@ cudaError_t run_scan(ScanArgs a, const ScanSpace& s, bool backward, cudaStream_t
                                          : scan_kernel<VEC, R, 1, T>(backward);
     if constexpr (VEC == 4)
         if (backward && a.C >= kLongRow) kernel = scan_bwd_kernel<VEC, R, 1, Policy::kOrdinary, T>;
-    kernel<<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+    kernel<<<static_cast<unsigned>(grid) - a.first_task, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, cudaStream_t st) {
+cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, bool withhold,
+                          cudaStream_t st) {
     // rows of C channels start on a 16-byte (fp32) or 8-byte (bf16) boundary
     // when C is a multiple of 4; other sizes take one channel per lane, and
     // four times the rows (100000 x 155 bf16: 54 us, 93 with eight rows)
-    if (a.C % 4 != 0) return run_scan<1, 32, T>(a, s, backward, st);
-    return run_scan<4, 8, T>(a, s, backward, st);
+    if (a.C % 4 != 0) return run_scan<1, 32, T>(a, s, backward, withhold, st);
+    return run_scan<4, 8, T>(a, s, backward, withhold, st);
 }
 
-cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, kda_dtype_t dt,
-                          cudaStream_t st) {
-    return dt == KDA_DTYPE_BF16 ? dispatch_scan<__nv_bfloat16>(a, s, backward, st)
-                                : dispatch_scan<float>(a, s, backward, st);
+cudaError_t dispatch_scan(const ScanArgs& a, const ScanSpace& s, bool backward, bool withhold,
+                          kda_dtype_t dt, cudaStream_t st) {
+    return dt == KDA_DTYPE_BF16 ? dispatch_scan<__nv_bfloat16>(a, s, backward, withhold, st)
+                                : dispatch_scan<float>(a, s, backward, withhold, st);
 }
 
 }  // namespace
@@ -831,28 +844,33 @@ size_t scan_workspace_bytes(int total, int C, bool backward) {
 
 cudaError_t launch_scan_fwd(const void* x, const float* g, const float* h0, const int32_t* cu,
                             int T, int total, int N, int C, kda_dtype_t dt, void* h,
-                            float* final_state, float* entry, void* workspace, cudaStream_t st) {
+                            float* final_state, float* entry, void* workspace, cudaStream_t st,
+                            const ScanTimeout& timeout) {
     ScanArgs a{};
+    a.wait_ns = timeout.wait_ns;
     a.x = x; a.g = g; a.h0 = h0; a.cu = cu; a.T = T; a.total = total; a.N = N; a.C = C;
     a.h = h; a.final_state = final_state; a.entry = entry;
-    return dispatch_scan(a, carve_scan(workspace, total, C, false), false, dt, st);
+    return dispatch_scan(a, carve_scan(workspace, total, C, false), false, timeout.withhold, dt, st);
 }
 
 cudaError_t launch_scan_bwd(const void* x, const float* g, const float* h0, const void* dout,
                             const float* dfinal, const float* entry, const int32_t* cu, int T,
                             int total, int N, int C, kda_dtype_t dt, void* dx, float* dg,
-                            float* dh0, void* workspace, cudaStream_t st) {
+                            float* dh0, void* workspace, cudaStream_t st,
+                            const ScanTimeout& timeout) {
     ScanArgs a{};
+    a.wait_ns = timeout.wait_ns;
     a.x = x; a.g = g; a.h0 = h0; a.cu = cu; a.T = T; a.total = total; a.N = N; a.C = C;
     const ScanSpace s = carve_scan(workspace, total, C, entry == nullptr);
     if (!entry) {
         a.entry = s.entry;
-        const cudaError_t e = dispatch_scan(a, s, false, dt, st);
+        const cudaError_t e = dispatch_scan(a, s, false, timeout.withhold, dt, st);
         if (e != cudaSuccess) return e;
+        a.keep_status = 1;
     }
     a.entry = entry ? const_cast<float*>(entry) : s.entry;
     a.dout = dout; a.dfinal = dfinal; a.dx = dx; a.dg = dg; a.dh0 = dh0;
-    return dispatch_scan(a, s, true, dt, st);
+    return dispatch_scan(a, s, true, timeout.withhold && entry, dt, st);
 }
 
 cudaError_t launch_scan_step(const void* x, const float* g, const float* state_in,

@@ -52,7 +52,7 @@ EXPORTS = (
     "kda_linear_scan_bwd_workspace_size", "kda_linear_scan_fwd", "kda_linear_scan_bwd",
     "kda_linear_scan_step", "kda_fp8_pitch", "kda_add_rms_norm",
     "kda_add_rms_norm_bwd_workspace_size", "kda_add_rms_norm_bwd", "kda_quantize_fp8",
-    "kda_fp8_matmul", "kda_test_fp8_matmul_timeout", "kda_test_fp8_matmul_plan",
+    "kda_fp8_matmul", "kda_test_linear_scan_timeout", "kda_test_fp8_matmul_timeout", "kda_test_fp8_matmul_plan",
 )
 
 
@@ -114,6 +114,8 @@ _SIGS = {
     "kda_add_rms_norm_bwd": ([_vp] * 4 + [_i] * 3 + [ctypes.c_float] + [_vp] * 3 + [_sz, _vp], _i),
     "kda_quantize_fp8": ([_vp] + [_i] * 5 + [_vp] * 3, _i),
     "kda_fp8_matmul": ([_vp] * 4 + [_i] * 5 + [_vp] * 2, _i),
+    "kda_test_linear_scan_timeout": ([_vp] * 4 + [_i] * 4 + [_vp] * 3 +
+                                     [_sz, ctypes.c_ulonglong, _vp], _i),
     "kda_test_fp8_matmul_timeout": ([_vp] * 4 + [_i] * 5 + [_vp] + [_i] * 3 + [_vp], _i),
     "kda_test_fp8_matmul_plan": ([_i] * 5 + [_vp] * 2, _i),
 }
@@ -621,6 +623,21 @@ def kda_linear_scan_bwd(x, g, initial_state, dout, dfinal_state, entry_states, c
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     return _enqueue("kda_linear_scan_bwd", dev, stream, check, px, pg, ph0, pdo, pdf, pe, pcu, B,
                     T, num_seqs, H, d, code, pdx, pdg, pdh, pw, wb)
+
+
+def kda_test_linear_scan_timeout(x, g, dout, entry_states, T, H, d, dtype, out, dg, workspace,
+                                 wait_ns, workspace_bytes=None, stream=None, check=True) -> int:
+    """The recurrence (dout None) or its backward with one tile never run and the
+    waits for tiles bounded by wait_ns: exercises the bounded-wait error path
+    (kda_get_device_status then reports KDA_ERR_TIMEOUT).  Testing only."""
+    code = dtype_code(dtype)
+    typed = (_TORCH_OF[code],)
+    (px, pg, pd, pe, po, pdg, pw), dev = _args(
+        "kda_test_linear_scan_timeout", (x, typed), (g, _F32), (dout, typed),
+        (entry_states, _F32), (out, typed), (dg, _F32), (workspace, _ANY))
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    return _enqueue("kda_test_linear_scan_timeout", dev, stream, check, px, pg, pd, pe, T, H, d,
+                    code, po, pdg, pw, wb, wait_ns)
 
 
 def kda_linear_scan_step(x, g, state_in, state_out, h, N, H, d, dtype, stream=None,

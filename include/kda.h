@@ -688,6 +688,21 @@ kda_status_t kda_test_overlap_flag_timeout(const void* q, const void* k, const v
                                            int withheld_chunk, int withheld_head,
                                            unsigned long long flag_wait_ns, void* stream);
 
+/* kda_test_linear_scan_timeout: kda_linear_scan_fwd of one sequence of T > 256 tokens
+ * (dout NULL; out: h) or kda_linear_scan_bwd (out: dx), with the first tile of the
+ * call's first pass never run (the forward's first tokens; the backward's last ones,
+ * or, without entry_states, the first tokens of the pass that recomputes them) and
+ * every wait for another tile bounded by wait_ns (1 ns .. 2 s) instead of 2 s.  The
+ * tiles that need it give up and record KDA_ERR_TIMEOUT in the status word; outputs
+ * are unspecified, the next call on the same workspace starts clean.  Workspace as
+ * for those calls.  Not a computation: only tests need it.
+ */
+kda_status_t kda_test_linear_scan_timeout(const void* x, const float* g, const void* dout,
+                                          const float* entry_states, int T, int H, int d,
+                                          kda_dtype_t dtype, void* out, float* dg,
+                                          void* workspace, size_t workspace_bytes,
+                                          unsigned long long wait_ns, void* stream);
+
 /* kda_test_fp8_matmul_timeout: kda_fp8_matmul with block `withheld_block` (counted
  * over the CTA's output tiles) of CTA `withheld_cta` never loaded, and every wait
  * bounded by wait_tests (2^16 .. 2^26) looks at its barrier instead of 2^26.  The
