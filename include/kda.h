@@ -600,7 +600,12 @@ kda_status_t kda_linear_scan_step(const void* x, const float* g, const float* st
  *   [M, K] with a scale per row and block, b [N, K] with a scale per row
  *   (b_block_rows = 1) or per 128 rows (128).  The products inside a block of
  *   128 are added up on the tensor cores in fp32, the blocks in fp32; out
- *   [M, N] in out_dtype, one rounding.  With b a weight [out, in] it is the
+ *   [M, N] in out_dtype, one rounding.  The two scales of a block are multiplied
+ *   with each other first, in fp32, so that product has to be a normal number,
+ *   2^-126 to below 2^128, as it is for scales made of blocks whose largest
+ *   magnitudes lie between 2^-54 and 2^72.  Below that a block's part of the sum
+ *   loses bits or is 0, above it is infinite, or NaN where the block's sum is 0 (a
+ *   block of zeros gives 0 with any scales whose product is finite).  With b a weight [out, in] it is the
  *   projection of a; with b the transposed weight the gradient of a
  *   projection's input; with both operands transposed (K: tokens,
  *   b_block_rows 1) the gradient of its weight.  Any M >= 0, N >= 1, K >= 1.

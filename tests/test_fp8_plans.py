@@ -162,3 +162,35 @@ def test_tiles_whose_waits_give_up_are_nan(M, N, K, block, cta, withheld):
     got.zero_()
     kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out=got)
     assert torch.equal(got, want)
+
+
+# sizes of each kernel: without stages (8 and 16 rows), of changed places, 128 and 256
+# rows of b a tile, whole and split
+EDGE = [(5, 200, 300), (13, 200, 300), (16, 5000, 1100), (9, 300, 9000), (60, 200, 300),
+        (20, 1000, 4100), (2100, 4090, 300), (130, 1000, 14500)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block", [128, 1])
+@pytest.mark.parametrize("sa_log2,sb_log2", [(-63, -63), (-17, -109), (-109, -17), (63, 50), (-100, 119)])
+def test_scales_at_the_edges_of_their_range(sa_log2, sb_log2, block):
+    """Products of scales that are just normal numbers, and large ones, on codes whose
+    sums are small whole numbers: the result is exact."""
+    plans = set()
+    for M, N, K in EDGE:
+        gen = torch.Generator(device="cuda").manual_seed(M)
+        pitch, KB = kda.kda_fp8_pitch(K), -(-K // 128)
+
+        def codes(rows):
+            y = torch.zeros(rows, pitch, device="cuda")
+            y[:, :K] = torch.randint(-1, 2, (rows, K), generator=gen, device="cuda")
+            return y
+        a, b = codes(M), codes(N)
+        sa = torch.full((KB, M), 2.0 ** sa_log2, device="cuda")
+        sb = torch.full((KB, N if block == 1 else -(-N // 128)), 2.0 ** sb_log2, device="cuda")
+        out = kda.fp8_matmul(a.to(torch.float8_e4m3fn), sa, b.to(torch.float8_e4m3fn), sb, K=K,
+                             b_block_rows=block, out_dtype=torch.float32)
+        want = (a.double() @ b.double().t()) * 2.0 ** (sa_log2 + sb_log2)
+        assert torch.equal(out.double(), want)
+        plans.add(kda.kda_test_fp8_matmul_plan(M, N, K, block))
+    assert {rows for rows, _ in plans} == {-1, 0, 128, 256}
