@@ -1022,7 +1022,7 @@ kda_status_t kda_quantize_fp8(const void* x, int rows, int cols, kda_dtype_t dty
 static kda_status_t fp8_matmul(const void* a8, const float* a_scale, const void* b8,
                                const float* b_scale, int M, int N, int K, int b_block_rows,
                                kda_dtype_t out_dtype, void* out, void* stream,
-                               const kda::Fp8Timeout& timeout) {
+                               const kda::Fp8Withheld& withheld) {
     if (M < 0 || N < 1 || K < 1 || M > kMaxFp8Dim || N > kMaxFp8Dim || K > kMaxFp8Dim ||
         !dtype_ok(out_dtype))
         return KDA_ERR_INVALID_ARG;
@@ -1033,29 +1033,26 @@ static kda_status_t fp8_matmul(const void* a8, const float* a_scale, const void*
     if (!kda::fp8_matmul_available()) return KDA_ERR_UNSUPPORTED;
     return from_cuda(kda::launch_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows == 1,
                                             out_dtype, out, static_cast<cudaStream_t>(stream),
-                                            timeout));
+                                            withheld));
 }
 
 kda_status_t kda_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
                             const float* b_scale, int M, int N, int K, int b_block_rows,
                             kda_dtype_t out_dtype, void* out, void* stream) {
     return fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, out, stream,
-                      kda::Fp8Timeout());
+                      kda::Fp8Withheld());
 }
 
 kda_status_t kda_test_fp8_matmul_timeout(const void* a8, const float* a_scale, const void* b8,
                                          const float* b_scale, int M, int N, int K,
                                          int b_block_rows, kda_dtype_t out_dtype, void* out,
-                                         int withheld_cta, int withheld_block, int wait_tests,
-                                         void* stream) {
-    if (withheld_cta < 0 || withheld_block < 0 || wait_tests < (1 << 16) || wait_tests > (1 << 26))
-        return KDA_ERR_INVALID_ARG;
-    kda::Fp8Timeout timeout;
-    timeout.cta = withheld_cta;
-    timeout.block = withheld_block;
-    timeout.tests = wait_tests;
+                                         int withheld_cta, int withheld_block, void* stream) {
+    if (withheld_cta < 0 || withheld_block < 0) return KDA_ERR_INVALID_ARG;
+    kda::Fp8Withheld withheld;
+    withheld.cta = withheld_cta;
+    withheld.block = withheld_block;
     return fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, out, stream,
-                      timeout);
+                      withheld);
 }
 
 kda_status_t kda_test_fp8_matmul_plan(int M, int N, int K, int b_block_rows, int sms,

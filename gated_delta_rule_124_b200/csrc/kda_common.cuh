@@ -327,15 +327,15 @@ void fp8_matmul_plan(int M, int N, int K, bool b_rows, int sms, int* tile_rows, 
 cudaError_t launch_fp8_small(const void* a8, const float* a_scale, const void* b8,
                              const float* b_scale, int M, int N, int K, bool b_rows,
                              kda_dtype_t out_dt, void* out, cudaStream_t st);
-// A test of the product's bounded waits: CTA `cta` never loads its block `block`, and
-// a wait gives up after `tests` looks at its barrier (the default: some seconds).
-struct Fp8Timeout {
-    int cta = -1, block = -1, tests = 1 << 26;
+// A test of the product's bounded waits: CTA `cta` (-1: none) never loads its block
+// `block`, and waits give up after milliseconds instead of seconds.
+struct Fp8Withheld {
+    int cta = -1, block = -1;
 };
 cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
                               const float* b_scale, int M, int N, int K, bool b_rows,
                               kda_dtype_t out_dt, void* out, cudaStream_t st,
-                              const Fp8Timeout& timeout = Fp8Timeout());
+                              const Fp8Withheld& withheld = Fp8Withheld());
 // G_full[t, h, c] = g[t, h] (a head-uniform gate spread over dk channels)
 cudaError_t launch_spread_gate(const float* g, int total, int H, int dk, float* out,
                                cudaStream_t st);

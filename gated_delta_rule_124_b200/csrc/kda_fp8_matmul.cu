@@ -77,20 +77,24 @@ struct MatmulArgs {
     int M, N, KB, NB; // NB: columns of sb
     int out_bf16, out_wide;  // wide: out starts on 32 bytes
     int ntm, tiles, split;
-    Fp8Timeout timeout;
-    // The block that this CTA's loads leave out (-1: none; tests of the waits).
-    __device__ __forceinline__ int withheld() const {
-        return static_cast<int>(blockIdx.x) == timeout.cta ? timeout.block : -1;
-    }
+    Fp8Withheld withheld;
 };
+// The block that this CTA's loads leave out (-1: none).
+template <bool kTest>
+__device__ __forceinline__ int withheld(const MatmulArgs& a) {
+    return kTest && static_cast<int>(blockIdx.x) == a.withheld.cta ? a.withheld.block : -1;
+}
 
-// Bounded wait on a phase parity (some seconds at most).  A test before the loop
-// and a plain loop of tests: the waits of the threads that issue the products
-// are mostly for phases that are complete, and with only a loop (or one with a
-// clock and a sleep in it) such a wait took 140 to 250 cycles more.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const MatmulArgs& a) {
+// Bounded wait on a phase parity (some seconds at most; milliseconds in the kernels
+// that test the limit).  A test before the loop and a plain loop of tests: the waits
+// of the threads that issue the products are mostly for phases that are complete,
+// and with only a loop (or one with a clock and a sleep in it) such a wait took 140
+// to 250 cycles more.  The limit is a constant: as an argument of the launch it cost
+// 0.6 % with a scale per row of B.
+template <bool kTest>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     if (mbar_test_wait(bar, parity)) return true;
-    for (int i = 0; i < a.timeout.tests; ++i)
+    for (int i = 0; i < (kTest ? 1 << 18 : 1 << 26); ++i)
         if (mbar_test_wait(bar, parity)) return true;
     return false;
 }
@@ -384,7 +388,7 @@ struct FragSums {
     }
 };
 
-template <int BN, bool kRowScales>
+template <int BN, bool kRowScales, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                       const MatmulArgs a) {
@@ -433,16 +437,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             if (elect_one()) {
                 int it = 0;
-                const int withheld = a.withheld();
+                const int left_out = withheld<kTest>(a);
                 for (int tile = first; tile < a.tiles && !*fail; tile += step) {
                     const int m0 = tile % a.ntm * kRowsA, n0 = tile / a.ntm * BN;
                     for (int kb = kb0; kb < kb1; ++kb, ++it) {
                         const int s = it % ST;
-                        if (!wait(&empty[s], ((it / ST) & 1) ^ 1, a)) {
+                        if (!wait<kTest>(&empty[s], ((it / ST) & 1) ^ 1)) {
                             *fail = 1;
                             break;
                         }
-                        if (it == withheld) continue;
+                        if (it == left_out) continue;
                         uint8_t* st = stages + s * P::kStage;
                         mbar_arrive_expect_tx(&full[s], P::kStage);
                         tma_load_2d(st, &tma, &full[s], kb * 128, m0);
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // loads in flight land before the CTA may end (a no-op unless
                 // a wait gave up: the products have waited for every load)
                 for (int s = 0; s < ST && s < it; ++s)
-                    wait(&full[s], ((it - 1 - s) / ST) & 1, a);
+                    wait<kTest>(&full[s], ((it - 1 - s) / ST) & 1);
             }
         } else if (warp < 3) {
             if (elect_one()) {
@@ -464,11 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int h = HV == 2 ? warp - 1 : 0, u = it * HV + h;
                         if (HV == 1 && (u & 1) != warp - 1) continue;
                         const int s = it % ST, b = u % NB;
-                        if (!wait(&full[s], (it / ST) & 1, a)) {
+                        if (!wait<kTest>(&full[s], (it / ST) & 1)) {
                             *fail = 1;
                             break;
                         }
-                        if (!wait(&tempty[b], ((u / NB) & 1) ^ 1, a)) {
+                        if (!wait<kTest>(&tempty[b], ((u / NB) & 1) ^ 1)) {
                             *fail = 1;
                             break;
                         }
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // no product is in flight when the tensor memory goes back
-                if (last >= 0) wait(&tfull[last % NB], (last / NB) & 1, a);
+                if (last >= 0) wait<kTest>(&tfull[last % NB], (last / NB) & 1);
             }
         } else {
             // scales: the values of the next blocks (across tiles) are requested
@@ -531,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < GROUP; ++u) {
                     if (u >= count) break;
                     const int s = it % ST;
-                    if (!wait(&sempty[s], ((it / ST) & 1) ^ 1, a)) {
+                    if (!wait<kTest>(&sempty[s], ((it / ST) & 1) ^ 1)) {
                         *fail = 1;
                         break;
                     }
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sums.fill(0ull);
             for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                 const int u = HV == 1 ? it : it * HV + wg, b = u % NB, s = it % ST;
-                ok = __all_sync(0xffffffffu, wait(&tfull[b], (u / NB) & 1, a));
+                ok = __all_sync(0xffffffffu, wait<kTest>(&tfull[b], (u / NB) & 1));
                 if (!ok) {
                     *fail = 1;
                     break;
@@ -646,7 +650,7 @@ constexpr int kFewBuffers = 4;                              // of tensor memory
 constexpr uint32_t kFewSmem = 1024 + kFewStages * kFewStage;
 static_assert(kFewStages * kFewStage >= kFewRows * kRowsA * 4, "a partial tile fits the stages");
 
-template <bool kRowScales>
+template <bool kRowScales, bool kTest>
 __global__ void __launch_bounds__(kFewThreads)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
                    const MatmulArgs a) {
@@ -687,14 +691,14 @@ __global__ void __launch_bounds__(kFewThreads)
     if (warp == 0) {
         if (elect_one()) {
             int it = 0;
-            const int withheld = a.withheld();
+            const int left_out = withheld<kTest>(a);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST;
-                if (*fail || !wait(&empty[s], ((it / ST) & 1) ^ 1, a)) {
+                if (*fail || !wait<kTest>(&empty[s], ((it / ST) & 1) ^ 1)) {
                     *fail = 1;
                     break;
                 }
-                if (it == withheld) continue;
+                if (it == left_out) continue;
                 uint8_t* st = stages + s * kFewStage;
                 mbar_arrive_expect_tx(&full[s], kFewStage);
                 tma_load_2d(st, &tmw, &full[s], kb * 128, n0);
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(kFewThreads)
             }
             // loads in flight land before the stages are written again (a no-op
             // unless a wait gave up: the products have waited for every load)
-            for (int s = 0; s < ST && s < it; ++s) wait(&full[s], ((it - 1 - s) / ST) & 1, a);
+            for (int s = 0; s < ST && s < it; ++s) wait<kTest>(&full[s], ((it - 1 - s) / ST) & 1);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -710,7 +714,7 @@ __global__ void __launch_bounds__(kFewThreads)
             int it = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST, b = it % NB;
-                if (!wait(&full[s], (it / ST) & 1, a) || !wait(&tempty[b], ((it / NB) & 1) ^ 1, a)) {
+                if (!wait<kTest>(&full[s], (it / ST) & 1) || !wait<kTest>(&tempty[b], ((it / NB) & 1) ^ 1)) {
                     *fail = 1;
                     break;
                 }
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(kFewThreads)
                 mma_commit(&empty[s]);
             }
             // no product is in flight when the tensor memory goes back
-            if (it > 0) wait(&tfull[(it - 1) % NB], ((it - 1) / NB) & 1, a);
+            if (it > 0) wait<kTest>(&tfull[(it - 1) % NB], ((it - 1) / NB) & 1);
         }
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(kFewThreads)
             for (int u = 0; u < NB; ++u) {  // block u of these is in buffer u
                 const int kb = base + u, it = kb - kb0;
                 if (kb >= kb1 || !ok) break;
-                ok = __all_sync(0xffffffffu, wait(&tfull[u], (it / NB) & 1, a));
+                ok = __all_sync(0xffffffffu, wait<kTest>(&tfull[u], (it / NB) & 1));
                 if (!ok) {
                     *fail = 1;
                     break;
@@ -879,7 +883,9 @@ cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cu
     if (!map_bytes(&tma, a8, a.M, K, kRowsA) || !map_bytes(&tmb, b8, a.N, K, BN))
         return cudaErrorInvalidValue;
     const int ctas = a.split > 1 ? a.tiles * a.split : a.tiles < sms ? a.tiles : sms;
-    return launch(fp8_matmul_kernel<BN, kRowScales>, ctas, kThreads, P::kSmem, a.split, st, tma, tmb, a);
+    auto kernel = a.withheld.cta < 0 ? fp8_matmul_kernel<BN, kRowScales, false>
+                                     : fp8_matmul_kernel<BN, kRowScales, true>;
+    return launch(kernel, ctas, kThreads, P::kSmem, a.split, st, tma, tmb, a);
 }
 
 // Rows of B per tile and the split of K: the pair with the least time by a model
@@ -933,8 +939,9 @@ cudaError_t run_few(const void* a8, const void* b8, const MatmulArgs& a, int K, 
     CUtensorMap tmw, tmx;
     if (!map_bytes(&tmw, b8, a.N, K, kRowsA) || !map_bytes(&tmx, a8, a.M, K, kFewRows))
         return cudaErrorInvalidValue;
-    return launch(fp8_few_kernel<kRowScales>, a.tiles * a.split, kFewThreads, kFewSmem, a.split, st, tmw,
-                  tmx, a);
+    auto kernel = a.withheld.cta < 0 ? fp8_few_kernel<kRowScales, false>
+                                     : fp8_few_kernel<kRowScales, true>;
+    return launch(kernel, a.tiles * a.split, kFewThreads, kFewSmem, a.split, st, tmw, tmx, a);
 }
 
 // Which kernel a product takes.  bn: rows of B per tile of the first one; kFewRowsPlan:
@@ -961,10 +968,10 @@ void plan(int M, int N, int K, bool b_rows, int sms, int* bn, int* split) {
 
 cudaError_t matmul_with(int bn, int split, const void* a8, const float* a_scale, const void* b8,
                         const float* b_scale, int M, int N, int K, bool b_rows,
-                        kda_dtype_t out_dt, void* out, const Fp8Timeout& timeout, int sms,
+                        kda_dtype_t out_dt, void* out, const Fp8Withheld& withheld, int sms,
                         cudaStream_t st) {
     MatmulArgs a{};
-    a.timeout = timeout;
+    a.withheld = withheld;
     a.sa = a_scale;
     a.sb = b_scale;
     a.out = out;
@@ -1000,7 +1007,7 @@ void fp8_matmul_plan(int M, int N, int K, bool b_rows, int sms, int* tile_rows, 
 cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* b8,
                               const float* b_scale, int M, int N, int K, bool b_rows,
                               kda_dtype_t out_dt, void* out, cudaStream_t st,
-                              const Fp8Timeout& timeout) {
+                              const Fp8Withheld& withheld) {
     if (M == 0) return cudaSuccess;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1008,10 +1015,10 @@ cudaError_t launch_fp8_matmul(const void* a8, const float* a_scale, const void* 
     if (e != cudaSuccess) return e;
     int bn = 0, split = 1;
     plan(M, N, K, b_rows, sms, &bn, &split);
-    if (bn == kNoStagesPlan && timeout.cta >= 0) return cudaErrorNotSupported;  // (no waits)
+    if (bn == kNoStagesPlan && withheld.cta >= 0) return cudaErrorNotSupported;  // (no waits)
     if (bn == kNoStagesPlan)
         return launch_fp8_small(a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, st);
-    return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, timeout, sms,
+    return matmul_with(bn, split, a8, a_scale, b8, b_scale, M, N, K, b_rows, out_dt, out, withheld, sms,
                        st);
 }
 

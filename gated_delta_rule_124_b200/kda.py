@@ -116,7 +116,7 @@ _SIGS = {
     "kda_fp8_matmul": ([_vp] * 4 + [_i] * 5 + [_vp] * 2, _i),
     "kda_test_linear_scan_timeout": ([_vp] * 4 + [_i] * 4 + [_vp] * 3 +
                                      [_sz, ctypes.c_ulonglong, _vp], _i),
-    "kda_test_fp8_matmul_timeout": ([_vp] * 4 + [_i] * 5 + [_vp] + [_i] * 3 + [_vp], _i),
+    "kda_test_fp8_matmul_timeout": ([_vp] * 4 + [_i] * 5 + [_vp] + [_i] * 2 + [_vp], _i),
     "kda_test_fp8_matmul_plan": ([_i] * 5 + [_vp] * 2, _i),
 }
 
@@ -700,15 +700,14 @@ def kda_fp8_matmul(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, o
 
 
 def kda_test_fp8_matmul_timeout(a8, a_scale, b8, b_scale, M, N, K, b_block_rows, out_dtype, out,
-                                withheld_cta, withheld_block, wait_tests, stream=None,
-                                check=True) -> int:
-    """The product with one block of one CTA never loaded and the waits bounded by
-    wait_tests: exercises the bounded-wait error path (NaN).  Testing only."""
+                                withheld_cta, withheld_block, stream=None, check=True) -> int:
+    """The product with one block of one CTA never loaded and shorter waits: exercises
+    the bounded-wait error path (NaN).  Testing only."""
     code = dtype_code(out_dtype)
     (pa, ps, pb, pt, po), dev = _args("kda_test_fp8_matmul_timeout", (a8, _FP8), (a_scale, _F32),
                                       (b8, _FP8), (b_scale, _F32), (out, (_TORCH_OF[code],)))
     return _enqueue("kda_test_fp8_matmul_timeout", dev, stream, check, pa, ps, pb, pt, M, N, K,
-                    b_block_rows, code, po, withheld_cta, withheld_block, wait_tests)
+                    b_block_rows, code, po, withheld_cta, withheld_block)
 
 
 def kda_test_fp8_matmul_plan(M, N, K, b_block_rows, sms=148) -> tuple:

@@ -710,7 +710,7 @@ kda_status_t kda_test_linear_scan_timeout(const void* x, const float* g, const v
 
 /* kda_test_fp8_matmul_timeout: kda_fp8_matmul with block `withheld_block` (counted
  * over the CTA's output tiles) of CTA `withheld_cta` never loaded, and every wait
- * bounded by wait_tests (2^16 .. 2^26) looks at its barrier instead of 2^26.  The
+ * bounded by 2^18 looks at its barrier (milliseconds) instead of 2^26.  The
  * waits that need that block give up; the CTA waits for its own copies and products
  * in flight and writes NaN for the tile that lacks the block and for its later
  * tiles, every other tile as kda_fp8_matmul does.  A CTA or block that the call does
@@ -720,8 +720,7 @@ kda_status_t kda_test_linear_scan_timeout(const void* x, const float* g, const v
 kda_status_t kda_test_fp8_matmul_timeout(const void* a8, const float* a_scale, const void* b8,
                                          const float* b_scale, int M, int N, int K,
                                          int b_block_rows, kda_dtype_t out_dtype, void* out,
-                                         int withheld_cta, int withheld_block, int wait_tests,
-                                         void* stream);
+                                         int withheld_cta, int withheld_block, void* stream);
 
 /* kda_test_fp8_matmul_plan: the kernel that kda_fp8_matmul takes for a product of
  * these sizes on a device of `sms` SMs (no device is needed).  *tile_rows: rows of b

@@ -120,10 +120,9 @@ def test_timeout_hook_refusals():
     kbuild.build()
     fake = 1 << 20
     ok = dict(a8=fake, a_scale=fake, b8=fake, b_scale=fake, M=20, N=64, K=64, b_block_rows=128,
-              out_dtype="bf16", out=fake, withheld_cta=0, withheld_block=0, wait_tests=1 << 16,
-              stream=0, check=False)
-    for change in (dict(withheld_cta=-1), dict(withheld_block=-1), dict(wait_tests=(1 << 16) - 1),
-                   dict(wait_tests=(1 << 26) + 1), dict(out=None), dict(K=0)):
+              out_dtype="bf16", out=fake, withheld_cta=0, withheld_block=0, stream=0,
+              check=False)
+    for change in (dict(withheld_cta=-1), dict(withheld_block=-1), dict(out=None), dict(K=0)):
         assert kda.kda_test_fp8_matmul_timeout(**{**ok, **change}) == kda.KDA_ERR_INVALID_ARG, change
     assert kda.kda_test_fp8_matmul_timeout(**{**ok, "M": 0}) == kda.KDA_OK
 
@@ -141,8 +140,7 @@ def test_tiles_whose_waits_give_up_are_nan(M, N, K, block, cta, withheld):
     a8, sa, b8, sb = operands(M + K, M, N, K, block)
     want = kda.fp8_matmul(a8, sa, b8, sb, K=K, b_block_rows=block, out_dtype=torch.float32)
     got = torch.zeros_like(want)
-    kda.kda_test_fp8_matmul_timeout(a8, sa, b8, sb, M, N, K, block, "f32", got, cta, withheld,
-                                    1 << 18)
+    kda.kda_test_fp8_matmul_timeout(a8, sa, b8, sb, M, N, K, block, "f32", got, cta, withheld)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     rows, split = kda.kda_test_fp8_matmul_plan(M, N, K, block, sms)
     KB, ntm, bn = -(-K // 128), -(-M // 128), rows or 128
