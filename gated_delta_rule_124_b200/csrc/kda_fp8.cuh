@@ -1,7 +1,9 @@
 // 8-bit values with a scale per block of 128 (internal to libkda): e4m3 codes
-// y8 = round(x * 448 / amax) and the fp32 scale amax / 448 that gives x back,
-// amax the block's largest magnitude.  One rounding to 4 significant bits, at
-// most half a step (2^-4 of the value) off down to amax * 2^-15, where e4m3's
+// y8 = round(x * f) with f = 448 / amax and the fp32 scale amax / 448 that gives x
+// back, amax the block's largest magnitude.  f and x * f are fp32 numbers, so that a
+// value that lies exactly between two codes may take either (2 in 10,000 of normally
+// distributed bf16 values do not take the even one).  One rounding to 4 significant
+// bits, at most half a step (2^-4 of the value) off down to amax * 2^-15, where e4m3's
 // subnormal numbers begin.
 #pragma once
 

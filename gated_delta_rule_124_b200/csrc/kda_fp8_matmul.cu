@@ -26,10 +26,11 @@
 // With few tiles the K blocks are split over a cluster of up to 8 CTAs, which
 // add their partial tiles through distributed shared memory in a fixed order.
 //
-// Measured on a B200: 8192 x 4096 x 4096 in bf16 134 us (2.05 PFLOP/s; 158 in a
-// long run under the power cap), with a scale per row on both sides 4096 x 4096 x
-// 4099 in fp32 111 us (1.24 PFLOP/s); a block's products and sums take 1000 cycles
-// and the products alone 512.  Giving each half of a last, part-filled round of
+// Measured on a B200 (calls in a graph; one after another from Python, under the
+// power cap, in brackets): 8192 x 4096 x 4096 in bf16 129 to 136 us, about 2.05
+// PFLOP/s (158), with a scale per row on both sides 4096 x 4096 x 4099 in fp32 110 to
+// 120 us, about 1.2 PFLOP/s (130); a block's products and sums take 1000 cycles and
+// the products alone 512.  Giving each half of a last, part-filled round of
 // tiles to a CTA of its own gained nothing: a half takes a block as long.
 //
 // Every wait is bounded; a tile whose waits gave up, and every later one of its CTA,
@@ -889,12 +890,20 @@ cudaError_t run(const void* a8, const void* b8, MatmulArgs a, int K, int sms, cu
 }
 
 // Rows of B per tile and the split of K: the pair with the least time by a model
-// of B200 measurements (us): a block takes 0.39 with 128 rows and 0.54 with 256
-// (all SMs busy), joining a cluster's partial tiles 4 and 7.  K = 4096, N = 4096,
+// of B200 measurements (us, calls in a graph): a block takes 0.39 with 128 rows and
+// 0.54 with 256 (all SMs busy), joining a cluster's partial tiles 4 and 7.  K = 4096, N = 4096,
 // measured for 128, 256, 512, 1024 and 8192 rows of A: 128 rows of B split 4 ways
 // 12.0 (16.7 unsplit), 2 ways 15.2 (16.9), unsplit 17.6; 256 rows unsplit 22.3
 // (29.6 with 128) and 134 (174).  With a scale per row of B 0.53 and 0.83
 // (4096 x 4096 x 4099: 110 with 256 rows, 124 with 128).
+// Longer K, the best split with 128 and with 256 rows of B: 64 x 2048 x 14336 16.6 (4
+// ways) and 15.7 (8), 64 x 6144 x 8192 19.3 (2) and 17.7 (4), 256 x 5120 x 6144 22.4
+// (whole) and 20.4 (3), 128 x 7168 x 16384 33.7 (2) and 31.1 (4), 512 x 4096 x 14336
+// 44.8 (whole) and 38.7 (2), 128 x 4096 x 14336 19.9 (4) and 24.0 (4); scales per row
+// 1024 x 1024 x 16384 39.1 (2) and 33.4 (4), 512 x 4096 x 8192 36.1 (whole) and 34.9 (2).
+// Of 32 shapes of 32 to 2048 rows of A, K = 4096 to 16384, 28 got the best of the plans
+// below and four were 1 to 4 % off it (128 x 12288 x 8192: 31.0, best 29.8 whole with
+// 128 rows).
 // The CTAs of a cluster share one of the device's groups of SMs, whose sizes few
 // numbers divide: 148 SMs hold 45 clusters of three, 33 of four and 15 of eight (the
 // occupancy query's answers; 16 tiles split eight ways took two rounds, 15.6 for 64

@@ -19,9 +19,12 @@
 // dw is summed per thread over the CTA's rows, then over the CTAs in a second
 // kernel, in a fixed order.
 //
-// Measured on a B200 (of the copy rate of 6.53 TB/s), bf16: 16391 x 4096 with a
-// residual to 8 bits 73 us (98 %; 77 with loads marked as streaming), 16 rows 2.8;
-// backward of 8192 x 4096 46 us (89 %, 4 of it the second kernel).  Without the
+// Measured on a B200 (of the copy rate of 6.53 TB/s), bf16, calls in a graph: 16391 x
+// 4096 with a residual to 8 bits 74 us (98 %; 77 with loads marked as streaming; 82 a
+// call, one after another from Python), 16 rows 3.2 (15); fp32 153 (87 %); backward of
+// 8192 x 4096 47 us (88 %, 4 of it the second kernel; 51 from Python).  Few CTAs hold
+// short rows' backward back: 16384 x 2048 60 us (69 %), 32768 x 1024 95 (43 %), 32768 x
+// 512 83 (25 %).  Without the
 // request of the next row ahead of the reduction a row's loads would wait for the
 // row before.
 #include <cuda_bf16.h>
@@ -34,7 +37,8 @@
 namespace kda {
 namespace {
 
-// Row groups that sum their own dw: two CTAs for each of a B200's 148 SMs.
+// Row groups that sum their own dw: two CTAs for each of a B200's 148 SMs where a
+// CTA has one row (D > 1024), one or half a one where it has two or four.
 constexpr int kMaxParts = 296;
 
 template <int TPR>

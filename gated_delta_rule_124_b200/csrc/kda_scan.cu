@@ -44,9 +44,10 @@
 // inside each tile from the tile's entry state, which the forward keeps (one
 // fp32 row per 64 tokens).  x, g, dout in and dx, dg out, each once.
 //
-// Measured on a B200 (of the copy rate of 6.53 TB/s), bf16: forward of 65536 x
-// 4096 channels 415 us (79 %; 576 in fp32, 86 %), backward 667 (86 %; fp32 813);
-// 4096 x 4096 33 and 53; 262144 x 128 93 and 130; a step of 256 x 4096 2.5 us.
+// Measured on a B200 (of the copy rate of 6.53 TB/s), bf16, calls in a graph: forward
+// of 65536 x 4096 channels 414 us (79 %; 447 a call, one after another from Python; 576
+// in fp32, 86 %), backward 667 (86 %; fp32 813); 4096 x 4096 33 and 53 (both 90, 96 from
+// Python); 262144 x 128 93 and 130; a step of 256 x 4096 2.5 us (7).
 // Against the copy rate the look-back costs most: without it the long forward
 // took 350.
 #include <cuda_bf16.h>

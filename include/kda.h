@@ -571,7 +571,8 @@ kda_status_t kda_linear_scan_step(const void* x, const float* g, const float* st
  * columns of one row ([ceil(K / 128), R]) or of 128 rows ([ceil(K / 128),
  * ceil(R / 128)]); element (r, k) stands for code * scale of its block.  The
  * quantising calls take scale = amax / 448, amax the block's largest magnitude
- * (at least 2^-100), and round code = x * (448 / amax) to nearest.  A NaN
+ * (at least 2^-100), and round code = x * f to nearest, f = 448 / amax in fp32 (a
+ * value exactly between two codes may take either).  A NaN
  * stays a NaN and leaves its block's scale alone; a block that holds an
  * infinity stands for NaN.
  *
